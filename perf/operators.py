@@ -331,6 +331,23 @@ def _plain_conv_bwd(s):
     return out
 
 
+def _recurrence(a, u, first):
+    """h_t = a_t h_{t-1} + u_t along dim 1 from h_{-1} = first (or 0): neighbouring spans joined, twice
+    as long each time, in log2(T) passes over the whole tensors."""
+    h, a, d = u.clone(), a.clone(), 1
+    if first is not None:
+        h[:, 0] += a[:, 0] * first
+    while d < u.shape[1]:
+        h0, a0 = h, a
+        h = h0.clone()
+        h[:, d:].addcmul_(a0[:, d:], h0[:, :-d])
+        if 2 * d < u.shape[1]:
+            a = a0.clone()
+            a[:, d:] *= a0[:, :-d]
+        d *= 2
+    return h
+
+
 def _plain_scan_parts(s, T):
     """The steps, the decays and the inputs of the recurrence, and the states after every token."""
     c = s["case"]
@@ -344,13 +361,8 @@ def _plain_scan_parts(s, T):
     Bm = s["Bm"].float().view(B, T, G, 1, N)
     a = torch.exp(step[..., None] * s["A"])
     u = ((step * x).view(B, T, G, C // G, 1) * Bm).view(B, T, C, N)
-    h = torch.empty_like(u)
-    st = s["state_in"]
-    prev = u.new_zeros(B, C, N) if st is None else st
-    for t in range(T):
-        torch.addcmul(u[:, t], a[:, t], prev, out=h[:, t])
-        prev = h[:, t]
-    return x, raw, step, a, u, h, prev
+    h = _recurrence(a, u, s["state_in"])
+    return x, raw, step, a, u, h, h[:, -1]
 
 
 def _plain_scan(s):
@@ -387,11 +399,10 @@ def _plain_scan_bwd(s):
     dyg = dy.view(B, T, G, C // G, 1)
     out["dCm"] = (hg * dyg).sum(3)
     # lam_t = dy_t C_t + a_{t+1} lam_{t+1}, the gradient of the state after token t
-    lam = (dyg * Cm).view(B, T, C, N).clone()
-    carry = s["dstate_in"] if s["dstate_in"] is not None else torch.zeros_like(lam[:, 0])
-    for t in range(T - 1, -1, -1):
-        lam[:, t] += carry
-        carry = a[:, t] * lam[:, t]
+    back = torch.ones_like(a)
+    back[:, 1:] = a[:, 1:].flip(1)
+    lam = _recurrence(back, (dyg * Cm).view(B, T, C, N).flip(1), s["dstate_in"]).flip(1)
+    carry = a[:, 0] * lam[:, 0]
     lamg = lam.view(B, T, G, C // G, N)
     lb = (lamg * Bm).sum(-1).view(B, T, C)
     out["dBm"] = (lamg * (step * x).view(B, T, G, C // G, 1)).sum(3)
@@ -410,7 +421,7 @@ def _plain_scan_bwd(s):
     names = ["dx", "ddt", "dA", "dBm", "dCm", "dD", "ddt_bias"] + (["dz"] if s["z"] is not None else [])
     r = [out[n].to(s[n[1:]].dtype) for n in names]
     if s["state_in"] is not None:
-        r.append(carry.clone())
+        r.append(carry)
     return r
 
 
