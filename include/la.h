@@ -78,7 +78,12 @@ typedef enum {
     LA_OP_CAUSAL_NORM_FWD = 10,
     LA_OP_CAUSAL_NORM_BWD = 11,
     LA_OP_GATED_FWD = 12,
-    LA_OP_GATED_BWD = 13
+    LA_OP_GATED_BWD = 13,
+    LA_OP_SHORT_CONV_BWD = 14,        /* these five: la_mixer_workspace_size */
+    LA_OP_SELECTIVE_SCAN_FWD = 15,
+    LA_OP_SELECTIVE_SCAN_BWD = 16,
+    LA_OP_GROUP_NORM_FWD = 17,
+    LA_OP_GROUP_NORM_BWD = 18
 } la_op;
 
 /* Feature map of the state-form stages and of la_causal_norm_*: elu+1 with the
@@ -407,6 +412,161 @@ la_status la_state_bwd_kv(const void *k, const void *v, const float *dstate, voi
  * D must be 64 or 128.  No workspace.  Errors as for the other entry points. */
 la_status la_chunk_decay_step(const void *q, const void *k, const void *v, void *o, float *state,
                               const float *decay, int B, int H, int D, la_dtype dtype, void *stream);
+
+/* ---- operators around the token mixers -----------------------------------
+ * What the layers of the models that the "flash-linear-attention" README lists
+ * put around the recurrences above, and the selective recurrence itself.  The
+ * pages name layers and models only; the formulas are written out here.
+ *
+ * Conventions that differ from the attention ops: tensors may start at any
+ * address that is a multiple of their element size (16-byte aligned ones with
+ * widths in multiples of 16 bytes get the widest accesses); tensor sizes are
+ * not limited to 2^31 elements; parameters (weights, rates, biases, scales) and
+ * their gradients are fp32.  No output may overlap an input or another output
+ * unless its comment allows it.  In a padded batch `lengths` (int32 [B], device,
+ * or NULL) gives each sequence's length, taken as 0 or T where it lies outside
+ * [0, T]: rows behind the end are not read (they may hold anything, NaN
+ * included), outputs and gradients there are written as zeros, and states are
+ * those after the sequence's own last token. */
+
+/* Rotary positions on queries and keys.  Of every head's D entries the first R
+ * are taken in R/2 pairs, (x_i, x_{i+R/2}) in the half layout, (x_2i, x_2i+1)
+ * interleaved, and pair i of the token at position p is turned by the angle
+ * p f_i and multiplied by `magnitude`:
+ *      a' = m (a cos(p f_i) - b sin(p f_i)),   b' = m (a sin(p f_i) + b cos(p f_i));
+ * entries from R on are copied.  The backward turns by -p f_i (with the same
+ * magnitude): the gradient of the forward.  The angle is formed and reduced in
+ * 64 bits, so far positions lose nothing.
+ *  q, oq      [B,H,T,D] of `dtype`;  k, ok [B,Hk,T,D], both NULL for one tensor
+ *  freqs      [R/2] fp32 device array (la_rotary_frequencies fills a host one)
+ *  positions  device int64, [B,T] (positions_per_batch = 1) or [T] (= 0), any
+ *             sign; NULL: position of token t is start + t
+ * oq = q and ok = k (in place) are allowed.  R even, 2 <= R <= D <= 1024. */
+typedef enum { LA_ROTARY_HALF = 0, LA_ROTARY_INTERLEAVED = 1 } la_rotary_layout;
+
+la_status la_rotary_fwd(const void *q, const void *k, void *oq, void *ok, const float *freqs,
+                        const long long *positions, int positions_per_batch, long long start,
+                        la_rotary_layout layout, float magnitude, int B, int H, int Hk, int T, int D, int R,
+                        la_dtype dtype, void *stream);
+la_status la_rotary_bwd(const void *doq, const void *dok, void *dq, void *dk, const float *freqs,
+                        const long long *positions, int positions_per_batch, long long start,
+                        la_rotary_layout layout, float magnitude, int B, int H, int Hk, int T, int D, int R,
+                        la_dtype dtype, void *stream);
+
+/* Fills the HOST array freqs[R/2] (no GPU call): f_i = base^(-2i/R), then for
+ * contexts longer than the trained length, stretched by factor >= 1:
+ *  LA_ROTARY_SCALE_LINEAR    f_i / factor (positions interpolated)
+ *  LA_ROTARY_SCALE_NTK       base replaced by base factor^(R/(R-2)): the fastest
+ *                            pair is kept, the slowest stretched by factor (R > 2)
+ *  LA_ROTARY_SCALE_BY_PARTS  a pair that turns n_i = original_length f_i / (2 pi)
+ *                            times over the trained length keeps f_i for
+ *                            n_i >= beta_fast, gets f_i / factor for n_i <= beta_slow,
+ *                            and in between the mix linear in n_i
+ * (factor, and the last three arguments, are not looked at where the kind does
+ * not name them.) */
+typedef enum {
+    LA_ROTARY_SCALE_NONE = 0,
+    LA_ROTARY_SCALE_LINEAR = 1,
+    LA_ROTARY_SCALE_NTK = 2,
+    LA_ROTARY_SCALE_BY_PARTS = 3
+} la_rotary_scaling;
+
+la_status la_rotary_frequencies(float *freqs, int R, double base, la_rotary_scaling scaling, double factor,
+                                double original_length, double beta_fast, double beta_slow);
+
+/* Bytes of device workspace of a LA_OP_SHORT_CONV_BWD, LA_OP_SELECTIVE_SCAN_* or
+ * LA_OP_GROUP_NORM_* call (256-byte aligned; 0 if none, and for invalid
+ * arguments).  G: the scan's or the norm's groups (1 for the convolution); N: the
+ * scan's states per channel or the convolution's taps W (1 for the norm). */
+size_t la_mixer_workspace_size(la_op op, int B, int T, int C, int G, int N, la_dtype dtype);
+
+typedef enum { LA_ACT_NONE = 0, LA_ACT_SILU = 1 } la_activation;
+
+/* Short causal depthwise convolution, channels last, with an activation
+ * (SiLU, s sigma(s), or none):
+ *      s[b,t,c] = bias[c] + sum_{j<W} w[c,j] x[b,t-W+1+j,c],   y = act(s).
+ *  x, y       [B,T,C] of `dtype`;  w [C,W], bias [C] or NULL: fp32
+ *  state_in   [B,W-1,C] of `dtype`: the W-1 inputs before the first token, oldest
+ *             first (NULL: zeros)
+ *  state_out  [B,W-1,C] or NULL: the last W-1 inputs; may be state_in
+ *  lengths    see above
+ * 2 <= W <= 8.  la_short_conv_step is T = 1 ([B,C] tensors) and always takes and
+ * gives the state. */
+la_status la_short_conv_fwd(const void *x, const float *w, const float *bias, const void *state_in, void *y,
+                            void *state_out, const int *lengths, la_activation act, int B, int T, int C, int W,
+                            la_dtype dtype, void *stream);
+la_status la_short_conv_step(const void *x, const float *w, const float *bias, const void *state_in, void *y,
+                             void *state_out, la_activation act, int B, int C, int W, la_dtype dtype, void *stream);
+
+/* Gradients of the convolution given dy and, for training in segments, dstate_in
+ * [B,W-1,C], the gradient of state_out from the tokens after (NULL: zeros).
+ * dx [B,T,C], dstate_out [B,W-1,C] or NULL (the gradient of state_in) of `dtype`;
+ * dw [C,W], dbias [C] or NULL fp32, summed in a fixed order.
+ * Workspace: la_mixer_workspace_size(LA_OP_SHORT_CONV_BWD, B, T, C, 1, W, dtype). */
+la_status la_short_conv_bwd(const void *x, const float *w, const float *bias, const void *state_in, const void *dy,
+                            const void *dstate_in, void *dx, float *dw, float *dbias, void *dstate_out,
+                            const int *lengths, la_activation act, int B, int T, int C, int W, la_dtype dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Selective state space scan: for every channel c of group g = c / (C/G), with N
+ * states,
+ *      d_t = softplus(dt[t,c] + dt_bias[c])        (softplus = 0: dt + dt_bias)
+ *      h_t[n] = exp(d_t A[c,n]) h_{t-1}[n] + d_t x[t,c] Bm[t,g,n]
+ *      y[t,c] = (sum_n Cm[t,g,n] h_t[n] + D[c] x[t,c]) silu(z[t,c])
+ * (without z: no gate, without D: no skip term).
+ *  x, dt, z, y [B,T,C], Bm, Cm [B,T,G,N] of `dtype`; z may be NULL
+ *  A [C,N] fp32;  D, dt_bias [C] fp32 or NULL
+ *  state_in [B,C,N] fp32 or NULL (zeros);  state_out [B,C,N] fp32 or NULL: the state
+ *  after the last token; may be state_in
+ *  lengths  see above
+ * C a multiple of G; 1 <= N <= 64.  fp32 arithmetic and states.  Workspace:
+ * la_mixer_workspace_size(LA_OP_SELECTIVE_SCAN_FWD, ...) (0 unless the sequence is
+ * split to fill the GPU).  la_selective_scan_step is T = 1 (no T dimension in the
+ * tensors) and always takes and gives the state. */
+la_status la_selective_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                const float *D, const void *z, const float *dt_bias, const float *state_in, void *y,
+                                float *state_out, const int *lengths, int softplus, int B, int T, int C, int G, int N,
+                                la_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+la_status la_selective_scan_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                 const float *D, const void *z, const float *dt_bias, const float *state_in, void *y,
+                                 float *state_out, int softplus, int B, int C, int G, int N, la_dtype dtype,
+                                 void *stream);
+
+/* Gradients of the scan given dy and dstate_in [B,C,N] fp32, the gradient of
+ * state_out from the tokens after (NULL: zeros).  dx, ddt, dz (exactly when z is
+ * given) [B,T,C], dBm, dCm [B,T,G,N] of `dtype` (summed over the group's channels
+ * in fp32 and rounded once); dA [C,N], dD, ddt_bias [C] (NULL: not computed)
+ * fp32; dstate_out [B,C,N] fp32 or NULL: the gradient of state_in.  Sums run in a
+ * fixed order.  Workspace: la_mixer_workspace_size(LA_OP_SELECTIVE_SCAN_BWD, ...). */
+la_status la_selective_scan_bwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                const float *D, const void *z, const float *dt_bias, const float *state_in,
+                                const void *dy, const float *dstate_in, void *dx, void *ddt, float *dA, void *dBm,
+                                void *dCm, float *dD, void *dz, float *ddt_bias, float *dstate_out,
+                                const int *lengths, int softplus, int B, int T, int C, int G, int N, la_dtype dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Group normalisation with an activation, channels last: the C channels in G
+ * groups, mean and variance (of the values, not of a sample) over a group's
+ * channels and all T positions of a batch entry,
+ *      y[b,t,c] = act(gamma[c] (x[b,t,c] - mean[b,g]) rstd[b,g] + beta[c]),
+ *      rstd = 1 / sqrt(var + eps).
+ * With T = 1 and B rows it is the per-token norm over head groups that follows
+ * retention; with T = H W the norm of an image grid.
+ *  x, y        [B,T,C] of `dtype`; y may be x
+ *  gamma, beta [C] fp32, each NULL for 1 and 0
+ *  mean, rstd  [B,G] fp32 out, or NULL: what the backward takes
+ * C a multiple of G, eps > 0.  Workspace: la_mixer_workspace_size(
+ * LA_OP_GROUP_NORM_FWD, B, T, C, G, 1, dtype). */
+la_status la_group_norm_fwd(const void *x, const float *gamma, const float *beta, void *y, float *mean, float *rstd,
+                            float eps, la_activation act, int B, int T, int C, int G, la_dtype dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* dx [B,T,C] of `dtype` (may be dy), dgamma, dbeta [C] fp32 (each may be NULL)
+ * from dy and the forward's mean and rstd; sums run in a fixed order.
+ * Workspace: la_mixer_workspace_size(LA_OP_GROUP_NORM_BWD, ...). */
+la_status la_group_norm_bwd(const void *x, const void *dy, const float *mean, const float *rstd, const float *gamma,
+                            const float *beta, void *dx, float *dgamma, float *dbeta, la_activation act, int B, int T,
+                            int C, int G, la_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Reports, and clears, the fault word of this library's tensor-core kernels on
  * the current device.  Every wait inside those kernels is bounded (2 s); a wait

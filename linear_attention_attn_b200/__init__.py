@@ -10,6 +10,11 @@ or bfloat16, 16-byte aligned.  ``state`` tensors are float32 [B, H, D, D+1].
 When ``workspace`` is omitted, a torch uint8 buffer of la_workspace_size()
 bytes is allocated (torch's allocator is the only allocator involved).  When
 ``stream`` is omitted the current torch stream is used.
+
+The operators around the token mixers (la_rotary_*, la_short_conv_*,
+la_selective_scan_*, la_group_norm_*) take [B, H, T, D] or channels-last
+[B, T, C] tensors at any element-aligned address, fp32 parameters, and int32
+``lengths`` for padded batches; their kernels run on the tensors' device.
 """
 from __future__ import annotations
 
@@ -29,7 +34,8 @@ LA_F32, LA_F16, LA_BF16 = 0, 1, 2
 OPS = {"bidir_fwd": 0, "bidir_bwd": 1, "simple_fwd": 2, "simple_bwd": 3,
        "chunk_decay_fwd": 4, "chunk_decay_bwd": 5, "state_reduce": 6, "state_apply": 7,
        "state_bwd_q": 8, "state_bwd_kv": 9, "causal_norm_fwd": 10, "causal_norm_bwd": 11, "gated_fwd": 12,
-       "gated_bwd": 13}
+       "gated_bwd": 13, "short_conv_bwd": 14, "selective_scan_fwd": 15, "selective_scan_bwd": 16,
+       "group_norm_fwd": 17, "group_norm_bwd": 18}
 FEATURES = {"identity": 0, "elu1": 1, "norm": 2}
 STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_ALIGNMENT",
           4: "LA_ERR_WORKSPACE", 5: "LA_ERR_CUDA", 6: "LA_ERR_TIMEOUT"}
@@ -73,6 +79,24 @@ for _n in ("la_bidir_fwd", "la_simple_fwd", "la_bidir_bwd", "la_simple_bwd", "la
            "la_chunk_decay_scan", "la_state_reduce", "la_state_apply", "la_state_bwd_q", "la_state_bwd_kv",
            "la_causal_norm_fwd", "la_causal_norm_bwd", "la_feature_map_fwd", "la_feature_map_bwd", "la_gated_fwd",
            "la_gated_bwd"):
+    getattr(_lib, _n).restype = _I
+_LL, _D = ctypes.c_longlong, ctypes.c_double
+_lib.la_rotary_fwd.argtypes = [_P] * 6 + [_I, _LL, _I, _F] + [_I] * 7 + [_P]
+_lib.la_rotary_bwd.argtypes = _lib.la_rotary_fwd.argtypes
+_lib.la_rotary_frequencies.argtypes = [_P, _I, _D, _I, _D, _D, _D, _D]
+_lib.la_mixer_workspace_size.argtypes = [_I] * 7
+_lib.la_mixer_workspace_size.restype = _Z
+_lib.la_short_conv_fwd.argtypes = [_P] * 7 + [_I] * 6 + [_P]
+_lib.la_short_conv_step.argtypes = [_P] * 6 + [_I] * 5 + [_P]
+_lib.la_short_conv_bwd.argtypes = [_P] * 11 + [_I] * 6 + [_P, _Z, _P]
+_lib.la_selective_scan_fwd.argtypes = [_P] * 12 + [_I] * 7 + [_P, _Z, _P]
+_lib.la_selective_scan_step.argtypes = [_P] * 11 + [_I] * 6 + [_P]
+_lib.la_selective_scan_bwd.argtypes = [_P] * 21 + [_I] * 7 + [_P, _Z, _P]
+_lib.la_group_norm_fwd.argtypes = [_P] * 6 + [_F] + [_I] * 6 + [_P, _Z, _P]
+_lib.la_group_norm_bwd.argtypes = [_P] * 9 + [_I] * 6 + [_P, _Z, _P]
+for _n in ("la_rotary_fwd", "la_rotary_bwd", "la_rotary_frequencies", "la_short_conv_fwd", "la_short_conv_step",
+           "la_short_conv_bwd", "la_selective_scan_fwd", "la_selective_scan_step", "la_selective_scan_bwd",
+           "la_group_norm_fwd", "la_group_norm_bwd"):
     getattr(_lib, _n).restype = _I
 _lib.la_bidir_fwd_static.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]
 _lib.la_bidir_fwd_static.restype = _I
@@ -478,6 +502,267 @@ def la_state_bwd_kv(k, v, dstate, dk, dv, feature="elu1", stream=None):
     _full_state_check(dstate, B, H, D, k.device, "dstate")
     _check(_lib.la_state_bwd_kv(_ptr(k), _ptr(v), _ptr(dstate), _ptr(dk), _ptr(dv), B, H, T, D, _dtype_code(k),
                                 _feature(feature), _stream(stream, k.device)), "la_state_bwd_kv")
+
+
+# ---- operators around the token mixers ---------------------------------------------------
+
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+ACTIVATIONS = {"none": 0, "silu": 1}
+
+
+def _choice(table, key, what):
+    if key not in table:
+        raise ValueError("%s must be one of %s, got %r" % (what, sorted(table), key))
+    return table[key]
+
+
+def _want(t, name, shape, dtype, dev):
+    """Checks one tensor (None passes) and returns its address."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor %s on %s" % (name, dtype, tuple(shape), dev))
+    return t.data_ptr()
+
+
+def _cuda(t, name, dims):
+    """Device and dtype code of a call's first tensor."""
+    if not t.is_cuda or t.dim() != dims or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor of %d dimensions" % (name, dims))
+    return t.device, _dtype_code(t)
+
+
+def _mixer_workspace(op, B, T, C, G, N, dt, workspace, dev, stream):
+    if workspace is None:
+        need = _lib.la_mixer_workspace_size(OPS[op], B, T, C, G, N, dt)
+        if need == 0:
+            return None, 0, None
+        import torch
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)      # torch aligns to 512 bytes
+        else:
+            # from the pool of the stream that the kernels run on: its earlier users are done there
+            s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _run(name, dev, stream, *args):
+    """Calls the entry point with `args` and the stream, on the tensors' device."""
+    import torch
+    if stream is None:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        rc = getattr(_lib, name)(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(_lib, name)(*args, s)
+    if rc != 0:
+        raise LAError(rc, name)
+
+
+def la_mixer_workspace_size(op, B: int, T: int, C: int, G: int, N: int, dtype) -> int:
+    """Bytes of workspace of a short_conv_bwd (G = 1, N = taps), selective_scan_* or group_norm_* (N = 1) call."""
+    import torch
+    code = OPS[op] if isinstance(op, str) else int(op)
+    if isinstance(dtype, torch.dtype):
+        dtype = {torch.float32: LA_F32, torch.float16: LA_F16, torch.bfloat16: LA_BF16}[dtype]
+    return int(_lib.la_mixer_workspace_size(code, B, T, C, G, N, int(dtype)))
+
+
+def la_rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                          original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """The R/2 turning rates of la_rotary_* as a float32 CPU tensor (see include/la.h for the scalings)."""
+    import torch
+    if R < 2 or R % 2:
+        raise ValueError("R must be even and >= 2")
+    out = torch.empty(R // 2, dtype=torch.float32)
+    _check(_lib.la_rotary_frequencies(_ptr(out), R, float(base), _choice(ROTARY_SCALINGS, scaling, "scaling"),
+                                      float(factor), float(original_length), float(beta_fast), float(beta_slow)),
+           "la_rotary_frequencies")
+    return out
+
+
+def _rotary(name, q, k, oq, ok, freqs, positions, start, layout, magnitude, stream):
+    import torch
+    dev, dt = _cuda(q, "the first tensor", 4)
+    B, H, T, D = q.shape
+    Hk = 0
+    if (k is None) != (ok is None):
+        raise ValueError("k and its output must be given together")
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must be a [B, Hk, T, D] tensor")
+        Hk = k.shape[1]
+    ks = (B, Hk, T, D)
+    R = 2 * freqs.numel()
+    per_batch = 0
+    if positions is not None:
+        per_batch = 1 if positions.dim() == 2 else 0
+    _run(name, dev, stream, q.data_ptr(), _want(k, "k", ks, q.dtype, dev),
+         _want(oq, "the first output", q.shape, q.dtype, dev), _want(ok, "the second output", ks, q.dtype, dev),
+         _want(freqs, "freqs", (R // 2,), torch.float32, dev),
+         _want(positions, "positions", (B, T) if per_batch else (T,), torch.int64, dev), per_batch, start,
+         _choice(ROTARY_LAYOUTS, layout, "layout"), magnitude, B, H, Hk, T, D, R, dt)
+
+
+def la_rotary_fwd(q, k, oq, ok, freqs, positions=None, start: int = 0, layout: str = "half", magnitude: float = 1.0,
+                  stream=None):
+    """oq, ok <- q [B, H, T, D] and k [B, Hk, T, D] (or None) with the first 2 len(freqs) entries of every head
+    turned by position * freqs; positions is int64 [B, T] or [T] (None: start + t).  In place is allowed."""
+    _rotary("la_rotary_fwd", q, k, oq, ok, freqs, positions, start, layout, magnitude, stream)
+
+
+def la_rotary_bwd(doq, dok, dq, dk, freqs, positions=None, start: int = 0, layout: str = "half",
+                  magnitude: float = 1.0, stream=None):
+    """dq, dk <- gradients of sum(oq * doq) + sum(ok * dok) for la_rotary_fwd (dok, dk may be None)."""
+    _rotary("la_rotary_bwd", doq, dok, dq, dk, freqs, positions, start, layout, magnitude, stream)
+
+
+def la_short_conv_fwd(x, w, y, bias=None, state_in=None, state_out=None, lengths=None, activation: str = "silu",
+                      stream=None):
+    """y <- act(bias + causal convolution of x [B, T, C] with w [C, W]); states [B, W-1, C] hold the inputs before
+    the first and after the last token (state_out may be state_in).  See include/la.h."""
+    import torch
+    dev, dt = _cuda(x, "x", 3)
+    B, T, C = x.shape
+    W = w.shape[-1]
+    st, f32 = (B, W - 1, C), torch.float32
+    _run("la_short_conv_fwd", dev, stream, x.data_ptr(), _want(w, "w", (C, W), f32, dev),
+         _want(bias, "bias", (C,), f32, dev), _want(state_in, "state_in", st, x.dtype, dev),
+         _want(y, "y", x.shape, x.dtype, dev), _want(state_out, "state_out", st, x.dtype, dev),
+         _want(lengths, "lengths", (B,), torch.int32, dev), _choice(ACTIVATIONS, activation, "activation"), B, T, C,
+         W, dt)
+
+
+def la_short_conv_step(x, w, y, state_in, state_out=None, bias=None, activation: str = "silu", stream=None):
+    """One token, x and y [B, C]; state_out defaults to state_in (updated in place)."""
+    import torch
+    dev, dt = _cuda(x, "x", 2)
+    B, C = x.shape
+    W = w.shape[-1]
+    st, f32 = (B, W - 1, C), torch.float32
+    state_out = state_in if state_out is None else state_out
+    _run("la_short_conv_step", dev, stream, x.data_ptr(), _want(w, "w", (C, W), f32, dev),
+         _want(bias, "bias", (C,), f32, dev), _want(state_in, "state_in", st, x.dtype, dev),
+         _want(y, "y", x.shape, x.dtype, dev), _want(state_out, "state_out", st, x.dtype, dev),
+         _choice(ACTIVATIONS, activation, "activation"), B, C, W, dt)
+
+
+def la_short_conv_bwd(x, w, dy, dx, dw, bias=None, dbias=None, state_in=None, dstate_in=None, dstate_out=None,
+                      lengths=None, activation: str = "silu", workspace=None, stream=None):
+    """dx, dw (and dbias, dstate_out) <- gradients of sum(y * dy) + sum(state_out * dstate_in) for
+    la_short_conv_fwd; dstate_out is the gradient of state_in."""
+    import torch
+    dev, dt = _cuda(x, "x", 3)
+    B, T, C = x.shape
+    W = w.shape[-1]
+    st, f32 = (B, W - 1, C), torch.float32
+    wp, wn, _keep = _mixer_workspace("short_conv_bwd", B, T, C, 1, W, dt, workspace, dev, stream)
+    _run("la_short_conv_bwd", dev, stream, x.data_ptr(), _want(w, "w", (C, W), f32, dev),
+         _want(bias, "bias", (C,), f32, dev), _want(state_in, "state_in", st, x.dtype, dev),
+         _want(dy, "dy", x.shape, x.dtype, dev), _want(dstate_in, "dstate_in", st, x.dtype, dev),
+         _want(dx, "dx", x.shape, x.dtype, dev), _want(dw, "dw", (C, W), f32, dev),
+         _want(dbias, "dbias", (C,), f32, dev), _want(dstate_out, "dstate_out", st, x.dtype, dev),
+         _want(lengths, "lengths", (B,), torch.int32, dev), _choice(ACTIVATIONS, activation, "activation"), B, T, C,
+         W, dt, wp, wn)
+
+
+def _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, lead, dev):
+    """Addresses of the scan's inputs and its sizes; lead is (B, T) or (B,)."""
+    import torch
+    C, f32 = x.shape[-1], torch.float32
+    if Bm.dim() != len(lead) + 2:
+        raise ValueError("Bm must be a tensor of %d dimensions ending in [G, N]" % (len(lead) + 2))
+    G, N = Bm.shape[-2:]
+    bc, st = lead + (G, N), (lead[0], C, N)
+    ptrs = (x.data_ptr(), _want(dt, "dt", x.shape, x.dtype, dev), _want(A, "A", (C, N), f32, dev),
+            _want(Bm, "Bm", bc, x.dtype, dev), _want(Cm, "Cm", bc, x.dtype, dev), _want(D, "D", (C,), f32, dev),
+            _want(z, "z", x.shape, x.dtype, dev), _want(dt_bias, "dt_bias", (C,), f32, dev),
+            _want(state_in, "state_in", st, f32, dev))
+    return ptrs, C, G, N, bc, st
+
+
+def la_selective_scan_fwd(x, dt, A, Bm, Cm, y, D=None, z=None, dt_bias=None, state_in=None, state_out=None,
+                          lengths=None, softplus: bool = True, workspace=None, stream=None):
+    """y <- the selective state space scan of x [B, T, C] with steps dt [B, T, C], rates A [C, N] and projections
+    Bm, Cm [B, T, G, N]; states [B, C, N] float32 (state_out may be state_in).  See include/la.h."""
+    import torch
+    dev, code = _cuda(x, "x", 3)
+    B, T = x.shape[:2]
+    ptrs, C, G, N, _, st = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, (B, T), dev)
+    wp, wn, _keep = _mixer_workspace("selective_scan_fwd", B, T, C, G, N, code, workspace, dev, stream)
+    _run("la_selective_scan_fwd", dev, stream, *ptrs, _want(y, "y", x.shape, x.dtype, dev),
+         _want(state_out, "state_out", st, torch.float32, dev), _want(lengths, "lengths", (B,), torch.int32, dev),
+         1 if softplus else 0, B, T, C, G, N, code, wp, wn)
+
+
+def la_selective_scan_step(x, dt, A, Bm, Cm, y, state_in, state_out=None, D=None, z=None, dt_bias=None,
+                           softplus: bool = True, stream=None):
+    """One token: x, dt, z, y [B, C], Bm, Cm [B, G, N]; state_out defaults to state_in (updated in place)."""
+    import torch
+    dev, code = _cuda(x, "x", 2)
+    B = x.shape[0]
+    ptrs, C, G, N, _, st = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, (B,), dev)
+    out = ptrs[-1] if state_out is None else _want(state_out, "state_out", st, torch.float32, dev)
+    _run("la_selective_scan_step", dev, stream, *ptrs, _want(y, "y", x.shape, x.dtype, dev), out,
+         1 if softplus else 0, B, C, G, N, code)
+
+
+def la_selective_scan_bwd(x, dt, A, Bm, Cm, dy, dx, ddt, dA, dBm, dCm, D=None, dD=None, z=None, dz=None, dt_bias=None,
+                          ddt_bias=None, state_in=None, dstate_in=None, dstate_out=None, lengths=None,
+                          softplus: bool = True, workspace=None, stream=None):
+    """Gradients of sum(y * dy) + sum(state_out * dstate_in) for la_selective_scan_fwd; dstate_out is the gradient
+    of state_in.  dA, dD, ddt_bias and the states' gradients are float32."""
+    import torch
+    dev, code = _cuda(x, "x", 3)
+    B, T = x.shape[:2]
+    ptrs, C, G, N, bc, st = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, (B, T), dev)
+    f32 = torch.float32
+    wp, wn, _keep = _mixer_workspace("selective_scan_bwd", B, T, C, G, N, code, workspace, dev, stream)
+    _run("la_selective_scan_bwd", dev, stream, *ptrs, _want(dy, "dy", x.shape, x.dtype, dev),
+         _want(dstate_in, "dstate_in", st, f32, dev), _want(dx, "dx", x.shape, x.dtype, dev),
+         _want(ddt, "ddt", x.shape, x.dtype, dev), _want(dA, "dA", (C, N), f32, dev),
+         _want(dBm, "dBm", bc, x.dtype, dev), _want(dCm, "dCm", bc, x.dtype, dev), _want(dD, "dD", (C,), f32, dev),
+         _want(dz, "dz", x.shape, x.dtype, dev), _want(ddt_bias, "ddt_bias", (C,), f32, dev),
+         _want(dstate_out, "dstate_out", st, f32, dev), _want(lengths, "lengths", (B,), torch.int32, dev),
+         1 if softplus else 0, B, T, C, G, N, code, wp, wn)
+
+
+def la_group_norm_fwd(x, y, groups: int, gamma=None, beta=None, eps: float = 1e-5, activation: str = "none",
+                      mean=None, rstd=None, workspace=None, stream=None):
+    """y <- act(gamma * (x - mean) * rstd + beta) for x [B, T, C] with its C channels in `groups` groups; mean and
+    rstd [B, groups] float32 receive the statistics that the backward takes.  y may be x."""
+    import torch
+    dev, dt = _cuda(x, "x", 3)
+    B, T, C = x.shape
+    f32, bg = torch.float32, (B, groups)
+    wp, wn, _keep = _mixer_workspace("group_norm_fwd", B, T, C, groups, 1, dt, workspace, dev, stream)
+    _run("la_group_norm_fwd", dev, stream, x.data_ptr(), _want(gamma, "gamma", (C,), f32, dev),
+         _want(beta, "beta", (C,), f32, dev), _want(y, "y", x.shape, x.dtype, dev), _want(mean, "mean", bg, f32, dev),
+         _want(rstd, "rstd", bg, f32, dev), eps, _choice(ACTIVATIONS, activation, "activation"), B, T, C, groups, dt,
+         wp, wn)
+
+
+def la_group_norm_bwd(x, dy, dx, groups: int, mean, rstd, gamma=None, beta=None, dgamma=None, dbeta=None,
+                      activation: str = "none", workspace=None, stream=None):
+    """dx (may be dy), dgamma, dbeta <- gradients of sum(y * dy) for la_group_norm_fwd."""
+    import torch
+    dev, dt = _cuda(x, "x", 3)
+    B, T, C = x.shape
+    f32, bg = torch.float32, (B, groups)
+    wp, wn, _keep = _mixer_workspace("group_norm_bwd", B, T, C, groups, 1, dt, workspace, dev, stream)
+    _run("la_group_norm_bwd", dev, stream, x.data_ptr(), _want(dy, "dy", x.shape, x.dtype, dev),
+         _want(mean, "mean", bg, f32, dev), _want(rstd, "rstd", bg, f32, dev), _want(gamma, "gamma", (C,), f32, dev),
+         _want(beta, "beta", (C,), f32, dev), _want(dx, "dx", x.shape, x.dtype, dev),
+         _want(dgamma, "dgamma", (C,), f32, dev), _want(dbeta, "dbeta", (C,), f32, dev),
+         _choice(ACTIVATIONS, activation, "activation"), B, T, C, groups, dt, wp, wn)
 
 
 def la_status_string(status: int) -> str:

@@ -1,0 +1,641 @@
+// la_norm.cu -- group normalisation with an activation, channels last, and its gradient.
+//
+//   xh = (x - mean) rstd over a group's channels and all positions of a batch entry,
+//   a = gamma xh + beta,  y = act(a);
+//   g = dy act'(a):  dbeta = sum g,  dgamma = sum g xh,
+//   dx = rstd (gamma g - m0 - xh m1),  m0 = mean(gamma g),  m1 = mean(gamma g xh) over the group.
+//
+// Bound by HBM.  A group that fits a block's registers is read once (small kernels: a part of a
+// warp, a warp, or a block a group; mean first, then the squares about it).  A larger one takes two
+// launches over the same tiles of tokens, whole rows at a time: sums, then the result, the second
+// walking every tile backwards so that it begins with what the first left in L2 last.
+// Means and squares never meet as large sums: a thread sums about its own first value, and threads
+// and tiles are joined through their means, sum M2_i + n_i (mean_i - mean)^2, so a mean far above
+// the spread costs no precision.  Every sum runs in a fixed order.
+#include "la_mixer.cuh"
+
+namespace la {
+namespace {
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
+__device__ __forceinline__ float act_f(float a, int silu) { return silu ? a * sigmoid_f(a) : a; }
+__device__ __forceinline__ float act_grad(float a, int silu) {
+    if (!silu) return 1.f;
+    const float s = sigmoid_f(a);
+    return s * fmaf(a, 1.f - s, 1.f);
+}
+
+// ------------------------------------------------------- groups in registers --
+// L lanes a group (a power of two up to 32, or the whole block of kSmallBlock), each with up to K
+// vectors of V elements.
+constexpr int kSmallBlock = 256;
+
+// Sum over a group's L lanes; red has kSmallBlock / 32 floats and is free on return.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], int L, float (*red)[N]) {
+    for (int m = L > 32 ? 16 : L / 2; m > 0; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+    if (L <= 32) return;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[threadIdx.x >> 5][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSmallBlock / 32; ++w) v[i] += red[w][i];
+    }
+    __syncthreads();
+}
+
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kSmallBlock) norm_small_fwd(NormArgs a, int L, int nvec) {
+    __shared__ float red[kSmallBlock / 32][1];
+    const int cg = a.C / a.G, gl = cg / V, lane = threadIdx.x % L;
+    const long long group = (long long)blockIdx.x * (kSmallBlock / L) + threadIdx.x / L;
+    const bool live = group < (long long)a.B * a.G;
+    const int b = live ? (int)(group / a.G) : 0, g = live ? (int)(group - (long long)b * a.G) : 0;
+    const long long base = (long long)b * a.T * a.C + (long long)g * cg;
+    const T *x = (const T *)a.x + base;
+    float v[K][V], s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int e = lane + k * L, t = e / gl, c = (e - t * gl) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = 0.f;
+        if (live && e < nvec) {
+            ldv<V>(x + (long long)t * a.C + c, v[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[0] += v[k][i];
+        }
+    }
+    group_sum<1>(s, L, red);
+    const float count = (float)nvec * V, mean = s[0] / count;
+    s[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (live && lane + k * L < nvec)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[0] = fmaf(v[k][i] - mean, v[k][i] - mean, s[0]);
+    group_sum<1>(s, L, red);
+    const float rstd = 1.f / sqrtf(s[0] / count + a.eps);
+    if (!live) return;
+    if (lane == 0) {
+        if (a.mean) a.mean[group] = mean;
+        if (a.rstd) a.rstd[group] = rstd;
+    }
+    T *y = (T *)a.y + base;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int e = lane + k * L, t = e / gl, c = (e - t * gl) * V;
+        if (e < nvec) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int ch = g * cg + c + i;
+                const float ga = a.gamma ? a.gamma[ch] : 1.f, be = a.beta ? a.beta[ch] : 0.f;
+                o[i] = act_f(fmaf((v[k][i] - mean) * rstd, ga, be), a.silu);
+            }
+            stv<V>(y + (long long)t * a.C + c, o);
+        }
+    }
+}
+
+// T = 1: a group's lanes keep their channels and walk over the batch rows b0 .. b1, so dgamma and
+// dbeta gather in registers; part [splits][C] takes them.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kSmallBlock) norm_small_bwd(NormArgs a, int L, int nvec, int rows_per, float2 *part) {
+    __shared__ float red[kSmallBlock / 32][2];
+    const int cg = a.C / a.G, lane = threadIdx.x % L;
+    const int g = blockIdx.x * (kSmallBlock / L) + threadIdx.x / L;
+    const bool live = g < a.G;
+    const int b0 = blockIdx.y * rows_per, b1 = min(a.B, b0 + rows_per);
+    float ga[K][V], be[K][V], dga[K][V], dbe[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + k * L, ch = g * cg + e * V + i;
+            const bool in = live && e < nvec;
+            ga[k][i] = in && a.gamma ? a.gamma[ch] : 1.f;
+            be[k][i] = in && a.beta ? a.beta[ch] : 0.f;
+            dga[k][i] = dbe[k][i] = 0.f;
+        }
+    const float inv = 1.f / ((float)nvec * V);
+    for (int b = b0; b < b1; ++b) {
+        const long long base = (long long)b * a.C + (long long)g * cg;
+        const float mean = live ? a.mean_in[(long long)b * a.G + g] : 0.f;
+        const float rstd = live ? a.rstd_in[(long long)b * a.G + g] : 0.f;
+        float xh[K][V], gr[K][V], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int e = lane + k * L;
+#pragma unroll
+            for (int i = 0; i < V; ++i) xh[k][i] = gr[k][i] = 0.f;
+            if (live && e < nvec) {
+                ldv<V>((const T *)a.x + base + e * V, xh[k]);
+                ldv<V>((const T *)a.dy + base + e * V, gr[k]);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    xh[k][i] = (xh[k][i] - mean) * rstd;
+                    gr[k][i] *= act_grad(fmaf(xh[k][i], ga[k][i], be[k][i]), a.silu);
+                    dbe[k][i] += gr[k][i];
+                    dga[k][i] = fmaf(gr[k][i], xh[k][i], dga[k][i]);
+                    gr[k][i] *= ga[k][i];
+                    s[0] += gr[k][i];
+                    s[1] = fmaf(gr[k][i], xh[k][i], s[1]);
+                }
+            }
+        }
+        group_sum<2>(s, L, red);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int e = lane + k * L;
+            if (live && e < nvec) {
+                float o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = rstd * (gr[k][i] - s[0] * inv - xh[k][i] * (s[1] * inv));
+                stv<V>((T *)a.dx + base + e * V, o);
+            }
+        }
+    }
+    if (!live || !part) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int e = lane + k * L;
+        if (e < nvec)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                part[(long long)blockIdx.y * a.C + g * cg + e * V + i] = make_float2(dga[k][i], dbe[k][i]);
+    }
+}
+
+// dgamma, dbeta from `parts` rows of [C] pairs: 32 channels a block, the warps over the rows.
+__device__ __forceinline__ void join_channels(const float2 *part, int parts, int C, int block, float *dgamma,
+                                              float *dbeta) {
+    __shared__ float2 red[16][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int c = block * 32 + lane;
+    float2 s = make_float2(0.f, 0.f);
+    if (c < C)
+        for (int p = warp; p < parts; p += warps) {
+            const float2 v = part[(long long)p * C + c];
+            s.x += v.x;
+            s.y += v.y;
+        }
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < C) {
+        for (int w = 1; w < warps; ++w) {
+            s.x += red[w][lane].x;
+            s.y += red[w][lane].y;
+        }
+        if (dgamma) dgamma[c] = s.x;
+        if (dbeta) dbeta[c] = s.y;
+    }
+}
+
+__global__ void __launch_bounds__(512) norm_join(const float2 *part, int parts, int C, float *dgamma, float *dbeta) {
+    join_channels(part, parts, C, blockIdx.x, dgamma, dbeta);
+}
+
+// --------------------------------------------------------------- tiled groups --
+// A block: one batch entry, one tile of tokens, one chunk of whole groups.  Its threads lie along
+// the chunk's `w` channel vectors, in `rows` rows of tokens; a single group wider than the block
+// is walked in strides (rows = 1).
+constexpr int kTiledBlock = 512;
+
+struct Tiling {
+    int gl, gpc, chunks, w, rows, threads, tiles, len;
+};
+
+__device__ __forceinline__ void whereabouts(const Tiling &q, long long block, int &chunk, int &tile, int &b) {
+    chunk = (int)(block % q.chunks);
+    block /= q.chunks;
+    tile = (int)(block % q.tiles);
+    b = (int)(block / q.tiles);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kTiledBlock) norm_stats(NormArgs a, Tiling q, float2 *part) {
+    __shared__ float s_n[kTiledBlock], s_mean[kTiledBlock], s_m2[kTiledBlock];
+    int chunk, tile, b;
+    whereabouts(q, blockIdx.x, chunk, tile, b);
+    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
+    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
+    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
+    const T *x = (const T *)a.x + (long long)b * a.T * a.C + (long long)g0 * cg;
+    float n = 0.f, s = 0.f, m2 = 0.f, pivot = 0.f;
+    if (r < q.rows && t0 + r < t1)
+        for (int v = v0; v < w; v += q.threads) {
+            if (n == 0.f) pivot = to_f(x[(long long)(t0 + r) * a.C + v * V]);
+#pragma unroll 8
+            for (int t = t0 + r; t < t1; t += q.rows) {
+                float e[V];
+                ldv<V>(x + (long long)t * a.C + v * V, e);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = e[i] - pivot;
+                    s += d;
+                    m2 = fmaf(d, d, m2);
+                }
+                n += V;
+            }
+        }
+    s_n[threadIdx.x] = n;
+    s_mean[threadIdx.x] = n > 0.f ? pivot + s / n : 0.f;
+    s_m2[threadIdx.x] = n > 0.f ? m2 - s * (s / n) : 0.f;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, members = q.rows * min(q.gl, q.threads);
+    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
+        float cnt = 0.f, sm = 0.f, sq = 0.f;
+        for (int e = lane; e < members; e += 32) {
+            const int er = e / min(q.gl, q.threads), id = er * q.w + j * q.gl + (e - er * min(q.gl, q.threads));
+            cnt += s_n[id];
+            sm = fmaf(s_n[id], s_mean[id], sm);
+        }
+        cnt = warp_sum(cnt);
+        const float mean = warp_sum(sm) / cnt;
+        for (int e = lane; e < members; e += 32) {
+            const int er = e / min(q.gl, q.threads), id = er * q.w + j * q.gl + (e - er * min(q.gl, q.threads));
+            const float d = s_mean[id] - mean;
+            sq += fmaf(s_n[id] * d, d, s_m2[id]);
+        }
+        sq = warp_sum(sq);
+        if (lane == 0) part[((long long)b * q.tiles + tile) * a.G + g0 + j] = make_float2(mean, sq);
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kTiledBlock) norm_apply(NormArgs a, Tiling q, const float2 *part) {
+    __shared__ float s_mean[kTiledBlock], s_rstd[kTiledBlock];
+    int chunk, tile, b;
+    whereabouts(q, blockIdx.x, chunk, tile, b);
+    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
+    const int lane = threadIdx.x & 31;
+    const float total = (float)a.T * cg;
+    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
+        const float2 *p = part + (long long)b * q.tiles * a.G + g0 + j;
+        float sm = 0.f, sq = 0.f;
+        for (int i = lane; i < q.tiles; i += 32)
+            sm = fmaf((float)min(q.len, a.T - i * q.len) * cg, p[(long long)i * a.G].x, sm);
+        const float mean = warp_sum(sm) / total;
+        for (int i = lane; i < q.tiles; i += 32) {
+            const float2 v = p[(long long)i * a.G];
+            const float d = v.x - mean;
+            sq += fmaf((float)min(q.len, a.T - i * q.len) * cg * d, d, v.y);
+        }
+        const float rstd = 1.f / sqrtf(fmaxf(warp_sum(sq), 0.f) / total + a.eps);
+        if (lane == 0) {
+            s_mean[j] = mean;
+            s_rstd[j] = rstd;
+            if (tile == 0) {
+                if (a.mean) a.mean[(long long)b * a.G + g0 + j] = mean;
+                if (a.rstd) a.rstd[(long long)b * a.G + g0 + j] = rstd;
+            }
+        }
+    }
+    __syncthreads();
+    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
+    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
+    if (r >= q.rows || t0 + r >= t1) return;
+    const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
+    const int last = t0 + r + (t1 - 1 - t0 - r) / q.rows * q.rows;
+    for (int v = v0; v < w; v += q.threads) {
+        const int j = v / q.gl;
+        const float mean = s_mean[j], rstd = s_rstd[j];
+        float ga[V], be[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = g0 * cg + v * V + i;
+            ga[i] = (a.gamma ? a.gamma[c] : 1.f) * rstd;
+            be[i] = a.beta ? a.beta[c] : 0.f;
+        }
+        const T *x = (const T *)a.x + base + v * V;
+        T *y = (T *)a.y + base + v * V;
+#pragma unroll 4
+        for (int t = last; t >= t0; t -= q.rows) {
+            float e[V];
+            ldv<V>(x + (long long)t * a.C, e);
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = act_f(fmaf(e[i] - mean, ga[i], be[i]), a.silu);
+            stv<V>(y + (long long)t * a.C, e);
+        }
+    }
+}
+
+// Sums of a tile: chan [B tiles][C] (sum g xh, sum g), part [B tiles][G] (sum gamma g, sum gamma g xh).
+template <typename T, int V>
+__global__ void __launch_bounds__(kTiledBlock) norm_bwd_sums(NormArgs a, Tiling q, float2 *part, float2 *chan) {
+    __shared__ float2 s_g[kTiledBlock];
+    extern __shared__ float2 s_c[];                       // [rows][w V], rows > 1
+    int chunk, tile, b;
+    whereabouts(q, blockIdx.x, chunk, tile, b);
+    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
+    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
+    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
+    const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
+    float2 *out = chan + ((long long)b * q.tiles + tile) * a.C + (long long)g0 * cg;
+    float2 grp = make_float2(0.f, 0.f);
+    if (r < q.rows)
+        for (int v = v0; v < w; v += q.threads) {
+            const int j = v / q.gl;
+            const float mean = a.mean_in[(long long)b * a.G + g0 + j], rstd = a.rstd_in[(long long)b * a.G + g0 + j];
+            float ga[V], be[V], dg[V], db[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = g0 * cg + v * V + i;
+                ga[i] = a.gamma ? a.gamma[c] : 1.f;
+                be[i] = a.beta ? a.beta[c] : 0.f;
+                dg[i] = db[i] = 0.f;
+            }
+            const T *x = (const T *)a.x + base + v * V, *dy = (const T *)a.dy + base + v * V;
+#pragma unroll 4
+            for (int t = t0 + r; t < t1; t += q.rows) {
+                float e[V], d[V];
+                ldv<V>(x + (long long)t * a.C, e);
+                ldv<V>(dy + (long long)t * a.C, d);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float xh = (e[i] - mean) * rstd;
+                    const float g = d[i] * act_grad(fmaf(xh, ga[i], be[i]), a.silu);
+                    db[i] += g;
+                    dg[i] = fmaf(g, xh, dg[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                grp.x = fmaf(ga[i], db[i], grp.x);
+                grp.y = fmaf(ga[i], dg[i], grp.y);
+                if (q.rows == 1) out[v * V + i] = make_float2(dg[i], db[i]);
+                else s_c[(r * q.w + v) * V + i] = make_float2(dg[i], db[i]);
+            }
+        }
+    s_g[threadIdx.x] = grp;
+    __syncthreads();
+    if (q.rows > 1)
+        for (int e = threadIdx.x; e < w * V; e += q.threads) {
+            float2 s = s_c[e];
+            for (int k = 1; k < q.rows; ++k) {
+                const float2 u = s_c[k * q.w * V + e];
+                s.x += u.x;
+                s.y += u.y;
+            }
+            out[e] = s;
+        }
+    const int lane = threadIdx.x & 31, gm = min(q.gl, q.threads), members = q.rows * gm;
+    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
+        float s0 = 0.f, s1 = 0.f;
+        for (int e = lane; e < members; e += 32) {
+            const int er = e / gm;
+            const float2 u = s_g[er * q.w + j * q.gl + (e - er * gm)];
+            s0 += u.x;
+            s1 += u.y;
+        }
+        s0 = warp_sum(s0);
+        s1 = warp_sum(s1);
+        if (lane == 0) part[((long long)b * q.tiles + tile) * a.G + g0 + j] = make_float2(s0, s1);
+    }
+}
+
+// dx; the blocks from `main_blocks` on join dgamma and dbeta instead.
+template <typename T, int V>
+__global__ void __launch_bounds__(kTiledBlock)
+norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, unsigned main_blocks) {
+    __shared__ float s_m0[kTiledBlock], s_m1[kTiledBlock];
+    if (blockIdx.x >= main_blocks) {
+        join_channels(chan, a.B * q.tiles, a.C, blockIdx.x - main_blocks, a.dgamma, a.dbeta);
+        return;
+    }
+    int chunk, tile, b;
+    whereabouts(q, blockIdx.x, chunk, tile, b);
+    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
+    const int lane = threadIdx.x & 31;
+    const float inv = 1.f / ((float)a.T * cg);
+    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
+        const float2 *p = part + (long long)b * q.tiles * a.G + g0 + j;
+        float s0 = 0.f, s1 = 0.f;
+        for (int i = lane; i < q.tiles; i += 32) {
+            const float2 v = p[(long long)i * a.G];
+            s0 += v.x;
+            s1 += v.y;
+        }
+        s0 = warp_sum(s0);
+        s1 = warp_sum(s1);
+        if (lane == 0) {
+            s_m0[j] = s0 * inv;
+            s_m1[j] = s1 * inv;
+        }
+    }
+    __syncthreads();
+    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
+    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
+    if (r >= q.rows || t0 + r >= t1) return;
+    const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
+    const int last = t0 + r + (t1 - 1 - t0 - r) / q.rows * q.rows;
+    for (int v = v0; v < w; v += q.threads) {
+        const int j = v / q.gl;
+        const float mean = a.mean_in[(long long)b * a.G + g0 + j], rstd = a.rstd_in[(long long)b * a.G + g0 + j];
+        const float m0 = s_m0[j], m1 = s_m1[j];
+        float ga[V], be[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = g0 * cg + v * V + i;
+            ga[i] = a.gamma ? a.gamma[c] : 1.f;
+            be[i] = a.beta ? a.beta[c] : 0.f;
+        }
+        const T *x = (const T *)a.x + base + v * V, *dy = (const T *)a.dy + base + v * V;
+        T *dx = (T *)a.dx + base + v * V;
+#pragma unroll 4
+        for (int t = last; t >= t0; t -= q.rows) {
+            float e[V], d[V];
+            ldv<V>(x + (long long)t * a.C, e);
+            ldv<V>(dy + (long long)t * a.C, d);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xh = (e[i] - mean) * rstd;
+                const float g = d[i] * act_grad(fmaf(xh, ga[i], be[i]), a.silu) * ga[i];
+                d[i] = rstd * (g - m0 - xh * m1);
+            }
+            stv<V>(dx + (long long)t * a.C, d);
+        }
+    }
+}
+
+// -------------------------------------------------------------------- choices --
+
+int pow2_at_least(long long n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+constexpr int kTileTarget = 2 * 148;       // blocks of a tiled launch: two of 512 threads an SM
+
+// Most tiles of a batch entry, whatever the access width.
+int most_tiles(int B, int T) {
+    const long long n = (kTileTarget + B - 1) / B;
+    return (int)(n < T ? n : T);
+}
+
+Tiling tiling(const NormArgs &a, int V) {
+    Tiling q;
+    q.gl = a.C / a.G / V;
+    const int fit = q.gl >= kTiledBlock ? 1 : kTiledBlock / q.gl < a.G ? kTiledBlock / q.gl : a.G;
+    q.chunks = (a.G + fit - 1) / fit;
+    q.gpc = (a.G + q.chunks - 1) / q.chunks;
+    q.chunks = (a.G + q.gpc - 1) / q.gpc;
+    q.w = q.gpc * q.gl;
+    q.rows = q.w >= kTiledBlock ? 1 : kTiledBlock / q.w;
+    if (q.rows > a.T) q.rows = a.T;
+    const int need = q.rows * q.w;
+    q.threads = need >= kTiledBlock ? kTiledBlock : (need + 31) / 32 * 32;
+    long long want = (kTileTarget + (long long)a.B * q.chunks - 1) / ((long long)a.B * q.chunks);
+    const long long most = (a.T + 4 * q.rows - 1) / (4 * q.rows);          // at least 4 tokens a thread
+    if (want > most) want = most;
+    q.len = (int)((a.T + want - 1) / want);
+    q.tiles = (a.T + q.len - 1) / q.len;
+    return q;
+}
+
+int width_for(const NormArgs &a) {
+    const uintptr_t bits = (uintptr_t)a.x | (uintptr_t)a.y | (uintptr_t)a.dy | (uintptr_t)a.dx;
+    return vec_width(elem_bytes(a.dt), (long long)(a.C / a.G), bits);
+}
+
+// A group of at most 2048 vectors fits a block's registers.  It is taken from there where its rows
+// are at least 64 bytes (T = 1 always: neighbouring groups share the sectors of one row) or the
+// whole tensor is small; else narrow rows would be fetched in part-used sectors.
+bool small_fwd(const NormArgs &a, int V) {
+    const long long nvec = (long long)a.T * (a.C / a.G) / V;
+    const size_t row = (size_t)(a.C / a.G) * elem_bytes(a.dt), all = (size_t)a.B * a.T * a.C * elem_bytes(a.dt);
+    return nvec <= 8 * kSmallBlock && (a.T == 1 || row >= 64 || all <= ((size_t)4 << 20));
+}
+
+void small_lanes(long long nvec, int *L, int *K) {
+    if (nvec <= 128) {
+        *L = nvec >= 32 ? 32 : pow2_at_least(nvec);
+        *K = pow2_at_least((nvec + *L - 1) / *L);
+    } else {
+        *L = kSmallBlock;
+        *K = pow2_at_least((nvec + kSmallBlock - 1) / kSmallBlock);
+    }
+}
+
+template <typename T, int V>
+la_status fwd_v(const NormArgs &a, cudaStream_t st) {
+    if (small_fwd(a, V)) {
+        const int nvec = a.T * (a.C / a.G) / V;
+        int L, K;
+        small_lanes(nvec, &L, &K);
+        const long long per = kSmallBlock / L;
+        const dim3 grid((unsigned)(((long long)a.B * a.G + per - 1) / per)), block(kSmallBlock);
+        switch (K) {
+        case 1: return launch("group_norm_fwd", norm_small_fwd<T, V, 1>, grid, block, 0, st, a, L, nvec);
+        case 2: return launch("group_norm_fwd", norm_small_fwd<T, V, 2>, grid, block, 0, st, a, L, nvec);
+        case 4: return launch("group_norm_fwd", norm_small_fwd<T, V, 4>, grid, block, 0, st, a, L, nvec);
+        default: return launch("group_norm_fwd", norm_small_fwd<T, V, 8>, grid, block, 0, st, a, L, nvec);
+        }
+    }
+    const Tiling q = tiling(a, V);
+    const dim3 grid((unsigned)((long long)a.B * q.tiles * q.chunks)), block(q.threads);
+    la_status rc = launch("group_norm_stats", norm_stats<T, V>, grid, block, 0, st, a, q, (float2 *)a.ws);
+    if (rc != LA_OK) return rc;
+    return launch("group_norm_fwd", norm_apply<T, V>, grid, block, 0, st, a, q, (const float2 *)a.ws);
+}
+
+// Batch rows a block of the T = 1 backward walks over: about four blocks an SM, at most 256 parts.
+int rows_per_block(int B, int G) {
+    long long splits = 4 * 148LL / ((G + 7) / 8) + 1;
+    if (splits > 256) splits = 256;
+    if (splits > B) splits = B;
+    return (int)((B + splits - 1) / splits);
+}
+
+// T = 1 with at most 16 channels a thread of a block (kept twice as sums, twice as values).
+bool small_bwd(int T, long long cg) { return T == 1 && cg <= 16 * kSmallBlock; }
+
+template <typename T, int V, int K>
+la_status small_bwd_k(const NormArgs &a, int L, int nvec, int per, float2 *part, cudaStream_t st) {
+    if constexpr (K * V <= 16) {
+        const dim3 grid((a.G + kSmallBlock / L - 1) / (kSmallBlock / L), (a.B + per - 1) / per);
+        return launch("group_norm_bwd", norm_small_bwd<T, V, K>, grid, dim3(kSmallBlock), 0, st, a, L, nvec, per, part);
+    } else {
+        return LA_ERR_UNSUPPORTED;       // K V <= 16 for every size that small_bwd admits
+    }
+}
+
+template <typename T, int V>
+la_status bwd_v(const NormArgs &a, cudaStream_t st) {
+    const bool join = a.dgamma || a.dbeta;
+    if (small_bwd(a.T, a.C / a.G)) {
+        const int nvec = a.C / a.G / V;
+        const int L = nvec > 64 ? kSmallBlock : nvec >= 32 ? 32 : pow2_at_least(nvec);
+        const int per = rows_per_block(a.B, a.G), splits = (a.B + per - 1) / per;
+        float2 *part = join ? (float2 *)a.ws : nullptr;
+        la_status rc;
+        switch (pow2_at_least((nvec + L - 1) / L)) {
+        case 1: rc = small_bwd_k<T, V, 1>(a, L, nvec, per, part, st); break;
+        case 2: rc = small_bwd_k<T, V, 2>(a, L, nvec, per, part, st); break;
+        case 4: rc = small_bwd_k<T, V, 4>(a, L, nvec, per, part, st); break;
+        case 8: rc = small_bwd_k<T, V, 8>(a, L, nvec, per, part, st); break;
+        default: rc = small_bwd_k<T, V, 16>(a, L, nvec, per, part, st); break;
+        }
+        if (rc != LA_OK || !join) return rc;
+        return launch("group_norm_bwd_join", norm_join, dim3((a.C + 31) / 32), dim3(512), 0, st, (const float2 *)part,
+                      splits, a.C, a.dgamma, a.dbeta);
+    }
+    const Tiling q = tiling(a, V);
+    float2 *part = (float2 *)a.ws, *chan = (float2 *)((char *)a.ws + up256(sizeof(float2) * a.B * q.tiles * a.G));
+    const unsigned blocks = (unsigned)((long long)a.B * q.tiles * q.chunks);
+    const size_t smem = q.rows > 1 ? sizeof(float2) * q.rows * q.w * V : 0;
+    la_status rc = launch("group_norm_bwd_sums", norm_bwd_sums<T, V>, dim3(blocks), dim3(q.threads), smem, st, a, q,
+                          part, chan);
+    if (rc != LA_OK) return rc;
+    return launch("group_norm_bwd", norm_bwd_apply<T, V>, dim3(blocks + (join ? (a.C + 31) / 32 : 0)),
+                  dim3(q.threads), 0, st, a, q, (const float2 *)part, (const float2 *)chan, blocks);
+}
+
+template <typename T>
+la_status norm_t(bool bwd, const NormArgs &a, cudaStream_t st) {
+    switch (width_for(a)) {
+    case 8: return bwd ? bwd_v<T, 16 / sizeof(T)>(a, st) : fwd_v<T, 16 / sizeof(T)>(a, st);
+    case 4: return bwd ? bwd_v<T, 4>(a, st) : fwd_v<T, 4>(a, st);
+    case 2: return bwd ? bwd_v<T, 2>(a, st) : fwd_v<T, 2>(a, st);
+    default: return bwd ? bwd_v<T, 1>(a, st) : fwd_v<T, 1>(a, st);
+    }
+}
+
+la_status norm_d(bool bwd, const NormArgs &a, cudaStream_t st) {
+    switch (a.dt) {
+    case LA_F32: return norm_t<float>(bwd, a, st);
+    case LA_F16: return norm_t<__half>(bwd, a, st);
+    default: return norm_t<__nv_bfloat16>(bwd, a, st);
+    }
+}
+
+}  // namespace
+
+size_t norm_fwd_workspace(int B, int T, int C, int G, la_dtype) {
+    if (T == 0 || (T == 1 && C / G <= 8 * kSmallBlock)) return 0;      // in registers at any access width
+    return up256(sizeof(float2) * B * most_tiles(B, T) * G);
+}
+
+size_t norm_bwd_workspace(int B, int T, int C, int G, la_dtype) {
+    if (T == 0) return 0;
+    const int per = rows_per_block(B, G), splits = (B + per - 1) / per;
+    if (small_bwd(T, C / G)) return up256(sizeof(float2) * splits * C);
+    return up256(sizeof(float2) * B * most_tiles(B, T) * G) + up256(sizeof(float2) * B * most_tiles(B, T) * C);
+}
+
+la_status norm_fwd(const NormArgs &a, cudaStream_t st) { return norm_d(false, a, st); }
+la_status norm_bwd(const NormArgs &a, cudaStream_t st) { return norm_d(true, a, st); }
+
+}  // namespace la
