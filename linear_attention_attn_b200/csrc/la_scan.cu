@@ -24,151 +24,194 @@ namespace {
 
 using namespace scan;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
 
 template <int LN> struct Cfg {
     static constexpr int width = kThreads / LN;             // channels a block
-    static constexpr int NP = kNS * LN;                     // padded states
-    static constexpr int per = kTile * width / kThreads;    // (token, channel) pairs a thread stages
-    static constexpr int bc_per = (kTile * NP + kThreads - 1) / kThreads;
-    static constexpr size_t smem = sizeof(float) * (2 * kTile * width * 2 + 2 * 2 * kTile * NP + 2 * kTile * width);
+    static constexpr int pairs = kTile * width;             // (token, channel)
+    static constexpr int quads = pairs / 4;                 // 4 channels of a token, staged by one thread
+    static constexpr int per = (quads + kThreads - 1) / kThreads;
+    static constexpr int bquads = kTile * LN;               // 4 states of a token's B (or C)
+    static constexpr int bper = (bquads + kThreads - 1) / kThreads;
+    static constexpr size_t smem = sizeof(f2) * (4 * pairs + 8 * kTile * LN) + sizeof(float) * 2 * pairs;
 };
 
 struct Seg {
     int segs, len;                 // segments of a sequence, tokens in each but the last (a multiple of kTile)
     float *S, *sum;                // [B, segs, C, N] end states, [B, segs, C] sums of d
+    int vec, bvec;                 // rows of x, dt, z, y (of Bm, Cm) allow accesses of 4 elements
 };
 
 // Tokens [t0, t1) of the block's channels from state h.  FULL: with outputs; else only h and sum of d.
 template <typename T, int LN, bool FULL>
-__device__ __forceinline__ void walk(const ScanArgs &a, const Place &p, int t0, int t1, const float (&A2)[kNS],
-                                     float (&h)[kNS], float &sum, float *smem) {
+__device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Place &p, int t0, int t1,
+                                     const f2 (&A2)[2], f2 (&h)[2], float &sum, float *smem) {
     using K = Cfg<LN>;
-    float2 *s_in = reinterpret_cast<float2 *>(smem);                  // [2][kTile][width]
-    float *s_B = smem + 2 * kTile * K::width * 2;                     // [2][kTile][NP]
-    float *s_C = s_B + 2 * kTile * K::NP;
-    float *s_y = s_C + 2 * kTile * K::NP;                             // [2][kTile][width]
+    // Every value that a pair of states shares is stored twice, side by side, and B and C in two
+    // planes of pairs, so that the inner loop reads 8 bytes a lane: such a read of at most 128
+    // different bytes a warp takes one pass through shared memory, a 16-byte one four.
+    f2 *s_d = reinterpret_cast<f2 *>(smem);                           // [2][kTile][width]: d, d
+    f2 *s_u = s_d + 2 * K::pairs;                                     // [2][kTile][width]: d x, d x
+    f2 *s_B = s_u + 2 * K::pairs;                                     // [2][kTile][2][LN]
+    f2 *s_C = s_B + 2 * kTile * 2 * LN;
+    float *s_y = reinterpret_cast<float *>(s_C + 2 * kTile * 2 * LN); // [2][kTile][width]
     const int tid = threadIdx.x, nl = tid % LN, ch = tid / LN;
     const int n = min(seq_end(a.lengths, p.b, a.T), t1);              // tokens that exist
     const int tiles = n > t0 ? (n - t0 + kTile - 1) / kTile : 0;
-    const long long row0 = (long long)p.b * a.T;
-    const T *x = (const T *)a.x, *dt = (const T *)a.dt_in, *z = (const T *)a.z;
-    const T *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm;
-
-    T rx[K::per], rd[K::per], rz[K::per], rB[K::bc_per], rC[K::bc_per];
+    const long long row0 = (long long)p.b * a.T + t0;
+    const bool vec = sg.vec, bvec = sg.bvec;
+    // a thread's quads are all of the same channels, in rows t_first, t_first + t_step, ...
+    constexpr int row = K::width / 4, t_step = kThreads / row, b_step = kThreads / LN;
+    static_assert(kThreads % row == 0, "");
+    const int c = tid % row * 4, have = p.nc - c, t_first = tid / row;
+    const int m = tid % LN * 4, b_have = a.N - m, b_first = tid / LN;
+    const long long x0 = (row0 + t_first) * a.C + p.c0 + c, xs = (long long)t_step * a.C;
+    const long long b0 = ((row0 + b_first) * a.G + p.g) * a.N + m, bs = (long long)b_step * a.G * a.N;
+    f2 bias[2], Dc[2];
+    {
+        float v[4], w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a.dt_bias && j < have ? a.dt_bias[p.c0 + c + j] : 0.f;
+            w[j] = FULL && a.D && j < have ? a.D[p.c0 + c + j] : 0.f;
+        }
+        bias[0] = pack2(v[0], v[1]);
+        bias[1] = pack2(v[2], v[3]);
+        Dc[0] = pack2(w[0], w[1]);
+        Dc[1] = pack2(w[2], w[3]);
+    }
+    Quad<T> rx[K::per], rd[K::per], rz[K::per], rB[K::bper], rC[K::bper];
     auto load = [&](int tile) {
-        const int tb = t0 + tile * kTile;
+        const long long xo = x0 + (long long)tile * kTile * a.C, bo = b0 + (long long)tile * kTile * a.G * a.N;
+        const int left = n - t0 - tile * kTile;                       // tokens from the tile's first on
 #pragma unroll
-        for (int i = 0; i < K::per; ++i) {
-            const int e = tid + i * kThreads, t = tb + e / K::width, c = e % K::width;
-            rx[i] = rd[i] = rz[i] = from_f<T>(0.f);
-            if (t < n && c < p.nc) {
-                const long long o = (row0 + t) * a.C + p.c0 + c;
-                rx[i] = x[o];
-                rd[i] = dt[o];
-                if (FULL && z) rz[i] = z[o];
+        for (int i = 0; i < K::per; ++i)
+            if (K::quads % kThreads == 0 || tid + i * kThreads < K::quads) {
+                const int live = t_first + i * t_step < left ? have : 0;
+                rx[i].load((const T *)a.x + xo + i * xs, live, vec);
+                rd[i].load((const T *)a.dt_in + xo + i * xs, live, vec);
+                if (FULL && a.z) rz[i].load((const T *)a.z + xo + i * xs, live, vec);
             }
-        }
 #pragma unroll
-        for (int i = 0; i < K::bc_per; ++i) {
-            const int e = tid + i * kThreads, t = tb + e / K::NP, m = e % K::NP;
-            rB[i] = rC[i] = from_f<T>(0.f);
-            if (e < kTile * K::NP && t < n && m < a.N) {
-                const long long o = ((row0 + t) * a.G + p.g) * a.N + m;
-                rB[i] = Bm[o];
-                if (FULL) rC[i] = Cm[o];
+        for (int i = 0; i < K::bper; ++i)
+            if (K::bquads % kThreads == 0 || tid + i * kThreads < K::bquads) {
+                const int live = b_first + i * b_step < left ? b_have : 0;
+                rB[i].load((const T *)a.Bm + bo + i * bs, live, bvec);
+                if (FULL) rC[i].load((const T *)a.Cm + bo + i * bs, live, bvec);
             }
-        }
     };
-    float skip[K::per], gate[K::per], skip2[K::per], gate2[K::per];   // of the tile at work, of the next
     auto stage = [&](int tile) {
-        const int buf = tile & 1, tb = t0 + tile * kTile;
+        const int buf = tile & 1, left = n - t0 - tile * kTile;
 #pragma unroll
-        for (int i = 0; i < K::per; ++i) {
-            const int e = tid + i * kThreads, t = tb + e / K::width, c = e % K::width;
-            float2 in = make_float2(0.f, 0.f);
-            skip2[i] = 0.f;
-            gate2[i] = 1.f;
-            if (t < n && c < p.nc) {
-                const float xv = to_f(rx[i]);
-                float d = to_f(rd[i]) + (a.dt_bias ? a.dt_bias[p.c0 + c] : 0.f);
-                if (a.softplus) d = softplus_f(d);
-                in = make_float2(d, d * xv);
-                if (FULL) {
-                    if (a.D) skip2[i] = a.D[p.c0 + c] * xv;
-                    if (z) {
-                        const float zv = to_f(rz[i]);
-                        gate2[i] = zv * sigmoid_f(zv);
-                    }
+        for (int i = 0; i < K::per; ++i)
+            if (K::quads % kThreads == 0 || tid + i * kThreads < K::quads) {
+                f2 d[2], x[2];
+                rd[i].values(d);
+                rx[i].values(x);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    d[j] = add2(d[j], bias[j]);
+                    if (a.softplus) d[j] = softplus2(d[j]);
+                    if (t_first + i * t_step >= left) d[j] = 0;       // behind the end: the state stays
+                    const f2 u = mul2(d[j], x[j]);
+                    float v0, v1, w0, w1;
+                    unpack2(d[j], v0, v1);
+                    unpack2(u, w0, w1);
+                    const int at = buf * K::pairs + 4 * (tid + i * kThreads) + 2 * j;
+                    *reinterpret_cast<ulonglong2 *>(s_d + at) = make_ulonglong2(both(v0), both(v1));
+                    *reinterpret_cast<ulonglong2 *>(s_u + at) = make_ulonglong2(both(w0), both(w1));
                 }
             }
-            s_in[buf * kTile * K::width + e] = in;
-        }
 #pragma unroll
-        for (int i = 0; i < K::bc_per; ++i) {
-            const int e = tid + i * kThreads;
-            if (e < kTile * K::NP) {
-                s_B[buf * kTile * K::NP + e] = to_f(rB[i]);
-                if (FULL) s_C[buf * kTile * K::NP + e] = to_f(rC[i]);
+        for (int i = 0; i < K::bper; ++i)
+            if (K::bquads % kThreads == 0 || tid + i * kThreads < K::bquads) {
+                f2 v[2];
+                const int at = (buf * kTile + b_first + i * b_step) * 2 * LN + tid % LN;
+                rB[i].values(v);
+                s_B[at] = v[0];
+                s_B[at + LN] = v[1];
+                if (FULL) {
+                    rC[i].values(v);
+                    s_C[at] = v[0];
+                    s_C[at + LN] = v[1];
+                }
             }
-        }
     };
     if (tiles > 0) {
         load(0);
         stage(0);
     }
+    __syncthreads();
     for (int tile = 0; tile < tiles; ++tile) {
-        __syncthreads();
         const int buf = tile & 1;
+        Quad<T> kx[K::per], kz[K::per];                       // this tile's, for its outputs
 #pragma unroll
         for (int i = 0; i < K::per; ++i) {
-            skip[i] = skip2[i];
-            gate[i] = gate2[i];
+            kx[i] = rx[i];
+            kz[i] = rz[i];
         }
         if (tile + 1 < tiles) load(tile + 1);
-        const float2 *in = s_in + buf * kTile * K::width + ch;
-        const float *sB = s_B + buf * kTile * K::NP + nl * kNS, *sC = s_C + buf * kTile * K::NP + nl * kNS;
-        float *sy = s_y + buf * kTile * K::width + ch;
+        const f2 *pd = s_d + buf * K::pairs + ch, *pu = s_u + buf * K::pairs + ch;
+        const f2 *pB = s_B + buf * kTile * 2 * LN + nl, *pC = s_C + buf * kTile * 2 * LN + nl;
+        // the sums stay in registers until the tile is done: a store to shared memory in between would
+        // keep the next tokens' loads from moving up
+        float ys[kTile / 4][4];
 #pragma unroll
         for (int q = 0; q < kTile; q += 4) {
-            float ys[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 v = in[(q + j) * K::width];
-                const float4 Bv = *reinterpret_cast<const float4 *>(sB + (q + j) * K::NP);
-                const float Bk[4] = {Bv.x, Bv.y, Bv.z, Bv.w};
-                if (!FULL) sum += v.x;
-#pragma unroll
-                for (int k = 0; k < kNS; ++k) h[k] = fmaf(ex2(v.x * A2[k]), h[k], v.y * Bk[k]);
+                const f2 d = pd[(q + j) * K::width], u = pu[(q + j) * K::width];
+                const f2 *B = pB + (q + j) * 2 * LN, *C = pC + (q + j) * 2 * LN;
+                h[0] = fma2(ex2_2(mul2(d, A2[0])), h[0], mul2(u, B[0]));
+                h[1] = fma2(ex2_2(mul2(d, A2[1])), h[1], mul2(u, B[LN]));
                 if (FULL) {
-                    const float4 Cv = *reinterpret_cast<const float4 *>(sC + (q + j) * K::NP);
-                    ys[j] = fmaf(Cv.x, h[0], fmaf(Cv.y, h[1], fmaf(Cv.z, h[2], Cv.w * h[3])));
+                    float y0, y1;
+                    unpack2(fma2(C[0], h[0], mul2(C[LN], h[1])), y0, y1);
+                    ys[q / 4][j] = y0 + y1;
+                } else {
+                    float d0, d1;
+                    unpack2(d, d0, d1);
+                    sum += d0;
                 }
             }
-            if (FULL) {
-                reduce4<LN>(ys, nl);
-                if (LN <= 4 || nl < 4) {
+            if (FULL) reduce4<LN>(ys[q / 4], nl);
+        }
+        if (FULL && (LN <= 4 || nl < 4)) {
+            float *sy = s_y + buf * K::pairs + ch + first_token<LN>(nl) * K::width;
 #pragma unroll
-                    for (int j = 0; j < Kept<LN>::value; ++j) sy[(q + first_token<LN>(nl) + j) * K::width] = ys[j];
-                }
-            }
+            for (int q = 0; q < kTile; q += 4)
+#pragma unroll
+                for (int j = 0; j < Kept<LN>::value; ++j) sy[(q + j) * K::width] = ys[q / 4][j];
         }
         if (tile + 1 < tiles) stage(tile + 1);
+        __syncthreads();
         if (FULL) {
-            __syncthreads();
+            const int left = n - t0 - tile * kTile, rows = t1 - t0 - tile * kTile;
+            T *y = (T *)a.y + x0 + (long long)tile * kTile * a.C;
 #pragma unroll
             for (int i = 0; i < K::per; ++i) {
-                const int e = tid + i * kThreads, t = t0 + tile * kTile + e / K::width, c = e % K::width;
-                if (t < t1 && c < p.nc)
-                    ((T *)a.y)[(row0 + t) * a.C + p.c0 + c] =
-                        from_f<T>(t < n ? (s_y[buf * kTile * K::width + e] + skip[i]) * gate[i] : 0.f);
+                if ((K::quads % kThreads == 0 || tid + i * kThreads < K::quads) && t_first + i * t_step < rows) {
+                    const ulonglong2 y2 = reinterpret_cast<const ulonglong2 *>(s_y + buf * K::pairs)[tid + i * kThreads];
+                    f2 o[2] = {y2.x, y2.y}, x[2], z[2];
+                    float v[4];
+                    kx[i].values(x);
+                    kz[i].values(z);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (a.D) o[j] = fma2(Dc[j], x[j], o[j]);
+                        if (a.z) o[j] = mul2(o[j], mul2(z[j], sigmoid2(z[j])));
+                        if (t_first + i * t_step >= left) o[j] = 0;
+                        unpack2(o[j], v[2 * j], v[2 * j + 1]);
+                    }
+                    store4(y + i * xs, v, have, vec);
+                }
             }
         }
     }
     if (FULL)
-        for (long long e = (long long)tiles * kTile * K::width + tid; e < (long long)(t1 - t0) * K::width; e += kThreads) {
-            const int t = t0 + (int)(e / K::width), c = (int)(e % K::width);
-            if (c < p.nc) ((T *)a.y)[(row0 + t) * a.C + p.c0 + c] = from_f<T>(0.f);
+        for (long long e = (long long)tiles * K::pairs + tid; e < (long long)(t1 - t0) * K::width; e += kThreads) {
+            const int t = (int)(e / K::width), cc = (int)(e % K::width);
+            if (cc < p.nc) ((T *)a.y)[(row0 + t) * a.C + p.c0 + cc] = from_f<T>(0.f);
         }
 }
 
@@ -185,48 +228,54 @@ scan_fwd_kernel(ScanArgs a, Seg sg, int tiles) {
     const int nl = threadIdx.x % LN, ch = threadIdx.x / LN, n0 = nl * kNS;
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
-    float A2[kNS] = {}, h[kNS] = {};
+    float A4[kNS] = {}, h4[kNS] = {};
     if (live) {
-        load_states(a.A + c * a.N, n0, a.N, A2);
+        load_states(a.A + c * a.N, n0, a.N, A4);
 #pragma unroll
-        for (int k = 0; k < kNS; ++k) A2[k] *= kLog2e;
+        for (int k = 0; k < kNS; ++k) A4[k] *= kLog2e;
     }
     const long long seg0 = ((long long)p.b * sg.segs) * a.C + c, seg_c = (long long)a.C;
     if (live) {
         if (PASS == 2) {
             // the state before this segment: segment 0's end, through the segments in between
-            load_states(sg.S + seg0 * a.N, n0, a.N, h);
+            load_states(sg.S + seg0 * a.N, n0, a.N, h4);
             for (int s = 1; s < p.seg; ++s) {
                 float S[kNS];
                 load_states(sg.S + (seg0 + s * seg_c) * a.N, n0, a.N, S);
                 const float d = sg.sum[seg0 + s * seg_c];
 #pragma unroll
-                for (int k = 0; k < kNS; ++k) h[k] = fmaf(ex2(d * A2[k]), h[k], S[k]);
+                for (int k = 0; k < kNS; ++k) h4[k] = fmaf(ex2(d * A4[k]), h4[k], S[k]);
             }
         } else if (p.seg == 0 && a.state_in) {
-            load_states(a.state_in + ((long long)p.b * a.C + c) * a.N, n0, a.N, h);
+            load_states(a.state_in + ((long long)p.b * a.C + c) * a.N, n0, a.N, h4);
         }
     }
     const int t0 = PASS == 0 ? 0 : p.seg * sg.len, t1 = PASS == 0 ? a.T : min(a.T, t0 + sg.len);
     float sum = 0.f;
+    const f2 A2[2] = {pack2(A4[0], A4[1]), pack2(A4[2], A4[3])};
+    f2 h[2] = {pack2(h4[0], h4[1]), pack2(h4[2], h4[3])};
     if (PASS != 1 || p.seg == 0)
-        walk<T, LN, true>(a, p, t0, t1, A2, h, sum, smem);
+        walk<T, LN, true>(a, sg, p, t0, t1, A2, h, sum, smem);
     else
-        walk<T, LN, false>(a, p, t0, t1, A2, h, sum, smem);
+        walk<T, LN, false>(a, sg, p, t0, t1, A2, h, sum, smem);
     if (!live) return;
+    unpack2(h[0], h4[0], h4[1]);
+    unpack2(h[1], h4[2], h4[3]);
     if (PASS == 1) {
-        store_states(sg.S + (seg0 + p.seg * seg_c) * a.N, n0, a.N, h);
+        store_states(sg.S + (seg0 + p.seg * seg_c) * a.N, n0, a.N, h4);
         if (nl == 0) sg.sum[seg0 + p.seg * seg_c] = sum;
     } else if (a.state_out && (PASS == 0 || p.seg == sg.segs - 1)) {
-        store_states(a.state_out + ((long long)p.b * a.C + c) * a.N, n0, a.N, h);
+        store_states(a.state_out + ((long long)p.b * a.C + c) * a.N, n0, a.N, h4);
     }
 }
 
+constexpr int kStepThreads = 128;
+
 // One token: LN lanes a channel; bound by the fp32 state, read and written once.
 template <typename T, int LN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kStepThreads)
 scan_step_kernel(ScanArgs a) {
-    const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long idx = (long long)blockIdx.x * kStepThreads + threadIdx.x;
     const long long bc = idx / LN;
     const int nl = (int)(idx % LN), n0 = nl * kNS;
     const bool live = bc < (long long)a.B * a.C;
@@ -267,12 +316,12 @@ scan_step_kernel(ScanArgs a) {
 }
 
 // Segments of the forward, from the sizes alone: one where the (batch, channel) blocks are at least
-// two an SM; else enough for about four an SM, each of at least 64 tokens.  Both passes run all
+// four an SM; else enough for about eight an SM, each of at least 64 tokens.  Both passes run all
 // segments but one at once, so fewer than 4 segments gain nothing.
 void fwd_segments(int B, int T, int C, int G, int N, int *segs, int *len) {
     const int width = kThreads / lanes_for(N);
     const long long blocks = (long long)B * G * ((C / G + width - 1) / width);
-    long long want = blocks >= 2 * 148 ? 1 : (4 * 148 + blocks - 1) / blocks;
+    long long want = blocks >= 4 * 148 ? 1 : (8 * 148 + blocks - 1) / blocks;
     if (want > T / 64) want = T / 64;
     if (want < 4) {
         *segs = 1;
@@ -290,6 +339,8 @@ la_status fwd_ln(const ScanArgs &a, cudaStream_t st) {
     fwd_segments(a.B, a.T, a.C, a.G, a.N, &sg.segs, &sg.len);
     sg.S = (float *)a.ws;
     sg.sum = sg.S + (size_t)a.B * sg.segs * a.C * a.N;
+    sg.vec = quad_rows<T>(a.C / a.G, a.x, a.dt_in, a.z, a.y);
+    sg.bvec = quad_rows<T>(a.N, a.Bm, a.Cm);
     const int tiles = (a.C / a.G + K::width - 1) / K::width;
     const unsigned blocks = (unsigned)((long long)a.B * a.G * tiles);
     if (sg.segs == 1)
@@ -316,8 +367,8 @@ la_status fwd_t(const ScanArgs &a, cudaStream_t st) {
 template <typename T, int LN>
 la_status step_ln(const ScanArgs &a, cudaStream_t st) {
     const long long n = (long long)a.B * a.C * LN;
-    return launch("selective_scan_step", scan_step_kernel<T, LN>, dim3((unsigned)((n + kThreads - 1) / kThreads)),
-                  dim3(kThreads), 0, st, a);
+    return launch("selective_scan_step", scan_step_kernel<T, LN>, 
+                  dim3((unsigned)((n + kStepThreads - 1) / kStepThreads)), dim3(kStepThreads), 0, st, a);
 }
 
 template <typename T>

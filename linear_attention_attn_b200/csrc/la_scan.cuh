@@ -20,7 +20,82 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ float softplus_f(float r) { return fmaxf(r, 0.f) + log1pf(expf(-fabsf(r))); }
+// Two fp32 operations at once on a register pair.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(ex2(a), ex2(b));
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ f2 both(float x) { return pack2(x, x); }
+
+// e^-|r| of a pair (0 from 128 on) with the argument's rounding repaired: r log2(e) as a product
+// and its remainder, and the part of log2(e) that one float leaves out.
+__device__ __forceinline__ f2 exp_neg_abs(f2 r) {
+    constexpr float rest = (float)(1.44269504088896340736 - (double)kLog2e);
+    float a, b;
+    unpack2(r, a, b);
+    const f2 m = pack2(fmaxf(-fabsf(a), -128.f), fmaxf(-fabsf(b), -128.f)), v = mul2(m, both(kLog2e));
+    const f2 lo = fma2(m, both(rest), fma2(m, both(kLog2e), mul2(v, both(-1.f))));
+    const f2 e = ex2_2(v);
+    return fma2(e, mul2(lo, both(0.69314718055994531f)), e);
+}
+// log(1 + e^r) = max(r, 0) + log1p(e), e = e^-|r| in (0, 1]: log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
+// by atanh's series up to s^13 (the next term is below 2^-26 of the sum).  A NaN stays one.
+__device__ __forceinline__ f2 softplus_from(f2 r, f2 e) {
+    float a, b, c, d;
+    unpack2(add2(e, both(2.f)), a, b);
+    const f2 s = mul2(e, pack2(rcp(a), rcp(b))), q = mul2(s, s);
+    f2 p = fma2(q, both(1.f / 13.f), both(1.f / 11.f));
+    p = fma2(q, p, both(1.f / 9.f));
+    p = fma2(q, p, both(1.f / 7.f));
+    p = fma2(q, p, both(1.f / 5.f));
+    p = fma2(q, p, both(1.f / 3.f));
+    p = fma2(q, p, both(1.f));
+    unpack2(r, a, b);
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(c) : "f"(a));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(d) : "f"(b));
+    return fma2(add2(s, s), p, pack2(c, d));
+}
+__device__ __forceinline__ f2 softplus2(f2 r) { return softplus_from(r, exp_neg_abs(r)); }
+__device__ __forceinline__ float softplus_f(float r) {
+    float a, b;
+    unpack2(softplus2(both(r)), a, b);
+    return a;
+}
+// 1 / (1 + e^-x) of a pair.
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+    float a, b;
+    unpack2(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
+    return pack2(rcp(a), rcp(b));
+}
 
 __device__ __forceinline__ int seq_end(const int *lengths, int b, int T) {
     return lengths ? min(max(lengths[b], 0), T) : T;
@@ -90,6 +165,67 @@ __device__ __forceinline__ void store_states(float *p, int n0, int N, const floa
         for (int k = 0; k < kNS; ++k)
             if (n0 + k < N) p[n0 + k] = h[k];
     }
+}
+
+// Four neighbouring elements of a row as they lie in memory, of which the first `have` exist (the
+// others 0).  vec: all or none do, and the address allows one access.  Kept as words, so that a load
+// is not waited for before its values are used.
+template <typename T, int SIZE = sizeof(T)> struct Quad;
+template <typename T> struct Quad<T, 2> {
+    uint2 w;
+    __device__ __forceinline__ void load(const T *p, int have, bool vec) {
+        w = make_uint2(0u, 0u);
+        if (vec) {
+            if (have >= 4) w = *reinterpret_cast<const uint2 *>(p);
+        } else {
+            const unsigned short *s = reinterpret_cast<const unsigned short *>(p);
+            if (have > 0) w.x = s[0];
+            if (have > 1) w.x |= (unsigned)s[1] << 16;
+            if (have > 2) w.y = s[2];
+            if (have > 3) w.y |= (unsigned)s[3] << 16;
+        }
+    }
+    __device__ __forceinline__ void values(f2 (&v)[2]) const {
+        Pack<T, 4> k;
+        *reinterpret_cast<uint2 *>(&k) = w;
+        v[0] = pack2(to_f(k.v[0]), to_f(k.v[1]));
+        v[1] = pack2(to_f(k.v[2]), to_f(k.v[3]));
+    }
+};
+template <typename T> struct Quad<T, 4> {
+    float4 w;
+    __device__ __forceinline__ void load(const T *p, int have, bool vec) {
+        w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec) {
+            if (have >= 4) w = *reinterpret_cast<const float4 *>(p);
+        } else {
+            if (have > 0) w.x = p[0];
+            if (have > 1) w.y = p[1];
+            if (have > 2) w.z = p[2];
+            if (have > 3) w.w = p[3];
+        }
+    }
+    __device__ __forceinline__ void values(f2 (&v)[2]) const {
+        v[0] = pack2(w.x, w.y);
+        v[1] = pack2(w.z, w.w);
+    }
+};
+template <typename T>
+__device__ __forceinline__ void store4(T *p, const float (&v)[4], int have, bool vec) {
+    if (vec && have >= 4) {
+        stv<4>(p, v);
+    } else if (!vec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < have) p[i] = from_f<T>(v[i]);
+    }
+}
+
+// Whether rows whose offsets are all multiples of `unit` elements allow accesses of 4 elements.
+template <typename T, typename... P>
+inline int quad_rows(int unit, P... p) {
+    const uintptr_t bits = (0 | ... | (uintptr_t)p);
+    return unit % 4 == 0 && (bits & (4 * sizeof(T) - 1)) == 0;
 }
 
 inline int lanes_for(int N) {
