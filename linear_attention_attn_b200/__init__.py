@@ -24,8 +24,8 @@ import os
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libla_b200.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError("libla_b200.so is not built: run `python -m linear_attention_attn_b200.build` "
+if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(_PKG, "_la_bind.so")):
+    raise ImportError("libla_b200.so and _la_bind.so are not built: run `python -m linear_attention_attn_b200.build` "
                       "(or __graft_entry__.build()) first")
 
 _lib = ctypes.CDLL(LIB_PATH)
@@ -505,66 +505,33 @@ def la_state_bwd_kv(k, v, dstate, dk, dv, feature="elu1", stream=None):
 
 
 # ---- operators around the token mixers ---------------------------------------------------
+# Their tensors go through csrc/la_bind.cpp, which checks them (ValueError), allocates the workspace
+# when none is passed and launches on the tensors' device; a refusing library raises LAError.
 
 ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 ACTIVATIONS = {"none": 0, "silu": 1}
 
+_bind = None
+
+
+def _load_bind():
+    global _bind
+    import torch  # noqa: F401  (the module links against torch's libraries)
+    from . import _la_bind
+    _bind = _la_bind
+    return _bind
+
 
 def _choice(table, key, what):
-    if key not in table:
+    code = table.get(key)
+    if code is None:
         raise ValueError("%s must be one of %s, got %r" % (what, sorted(table), key))
-    return table[key]
+    return code
 
 
-def _want(t, name, shape, dtype, dev):
-    """Checks one tensor (None passes) and returns its address."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor %s on %s" % (name, dtype, tuple(shape), dev))
-    return t.data_ptr()
-
-
-def _cuda(t, name, dims):
-    """Device and dtype code of a call's first tensor."""
-    if not t.is_cuda or t.dim() != dims or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous CUDA tensor of %d dimensions" % (name, dims))
-    return t.device, _dtype_code(t)
-
-
-def _mixer_workspace(op, B, T, C, G, N, dt, workspace, dev, stream):
-    if workspace is None:
-        need = _lib.la_mixer_workspace_size(OPS[op], B, T, C, G, N, dt)
-        if need == 0:
-            return None, 0, None
-        import torch
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)      # torch aligns to 512 bytes
-        else:
-            # from the pool of the stream that the kernels run on: its earlier users are done there
-            s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-            with torch.cuda.stream(s):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _run(name, dev, stream, *args):
-    """Calls the entry point with `args` and the stream, on the tensors' device."""
-    import torch
-    if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
-        rc = getattr(_lib, name)(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = getattr(_lib, name)(*args, s)
-    if rc != 0:
-        raise LAError(rc, name)
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def la_mixer_workspace_size(op, B: int, T: int, C: int, G: int, N: int, dtype) -> int:
@@ -589,130 +556,70 @@ def la_rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "none", 
     return out
 
 
-def _rotary(name, q, k, oq, ok, freqs, positions, start, layout, magnitude, stream):
-    import torch
-    dev, dt = _cuda(q, "the first tensor", 4)
-    B, H, T, D = q.shape
-    Hk = 0
-    if (k is None) != (ok is None):
-        raise ValueError("k and its output must be given together")
-    if k is not None:
-        if k.dim() != 4:
-            raise ValueError("k must be a [B, Hk, T, D] tensor")
-        Hk = k.shape[1]
-    ks = (B, Hk, T, D)
-    R = 2 * freqs.numel()
-    per_batch = 0
-    if positions is not None:
-        per_batch = 1 if positions.dim() == 2 else 0
-    _run(name, dev, stream, q.data_ptr(), _want(k, "k", ks, q.dtype, dev),
-         _want(oq, "the first output", q.shape, q.dtype, dev), _want(ok, "the second output", ks, q.dtype, dev),
-         _want(freqs, "freqs", (R // 2,), torch.float32, dev),
-         _want(positions, "positions", (B, T) if per_batch else (T,), torch.int64, dev), per_batch, start,
-         _choice(ROTARY_LAYOUTS, layout, "layout"), magnitude, B, H, Hk, T, D, R, dt)
-
-
 def la_rotary_fwd(q, k, oq, ok, freqs, positions=None, start: int = 0, layout: str = "half", magnitude: float = 1.0,
                   stream=None):
     """oq, ok <- q [B, H, T, D] and k [B, Hk, T, D] (or None) with the first 2 len(freqs) entries of every head
     turned by position * freqs; positions is int64 [B, T] or [T] (None: start + t).  In place is allowed."""
-    _rotary("la_rotary_fwd", q, k, oq, ok, freqs, positions, start, layout, magnitude, stream)
+    rc = (_bind or _load_bind()).rotary(0, q, k, oq, ok, freqs, positions, start,
+                                        _choice(ROTARY_LAYOUTS, layout, "layout"), magnitude, _handle(stream))
+    if rc:
+        raise LAError(rc, "la_rotary_fwd")
 
 
 def la_rotary_bwd(doq, dok, dq, dk, freqs, positions=None, start: int = 0, layout: str = "half",
                   magnitude: float = 1.0, stream=None):
     """dq, dk <- gradients of sum(oq * doq) + sum(ok * dok) for la_rotary_fwd (dok, dk may be None)."""
-    _rotary("la_rotary_bwd", doq, dok, dq, dk, freqs, positions, start, layout, magnitude, stream)
+    rc = (_bind or _load_bind()).rotary(1, doq, dok, dq, dk, freqs, positions, start,
+                                        _choice(ROTARY_LAYOUTS, layout, "layout"), magnitude, _handle(stream))
+    if rc:
+        raise LAError(rc, "la_rotary_bwd")
 
 
 def la_short_conv_fwd(x, w, y, bias=None, state_in=None, state_out=None, lengths=None, activation: str = "silu",
                       stream=None):
     """y <- act(bias + causal convolution of x [B, T, C] with w [C, W]); states [B, W-1, C] hold the inputs before
     the first and after the last token (state_out may be state_in).  See include/la.h."""
-    import torch
-    dev, dt = _cuda(x, "x", 3)
-    B, T, C = x.shape
-    W = w.shape[-1]
-    st, f32 = (B, W - 1, C), torch.float32
-    _run("la_short_conv_fwd", dev, stream, x.data_ptr(), _want(w, "w", (C, W), f32, dev),
-         _want(bias, "bias", (C,), f32, dev), _want(state_in, "state_in", st, x.dtype, dev),
-         _want(y, "y", x.shape, x.dtype, dev), _want(state_out, "state_out", st, x.dtype, dev),
-         _want(lengths, "lengths", (B,), torch.int32, dev), _choice(ACTIVATIONS, activation, "activation"), B, T, C,
-         W, dt)
+    rc = (_bind or _load_bind()).conv_fwd(x, w, bias, state_in, y, state_out, lengths,
+                                          _choice(ACTIVATIONS, activation, "activation"), _handle(stream))
+    if rc:
+        raise LAError(rc, "la_short_conv_fwd")
 
 
 def la_short_conv_step(x, w, y, state_in, state_out=None, bias=None, activation: str = "silu", stream=None):
     """One token, x and y [B, C]; state_out defaults to state_in (updated in place)."""
-    import torch
-    dev, dt = _cuda(x, "x", 2)
-    B, C = x.shape
-    W = w.shape[-1]
-    st, f32 = (B, W - 1, C), torch.float32
-    state_out = state_in if state_out is None else state_out
-    _run("la_short_conv_step", dev, stream, x.data_ptr(), _want(w, "w", (C, W), f32, dev),
-         _want(bias, "bias", (C,), f32, dev), _want(state_in, "state_in", st, x.dtype, dev),
-         _want(y, "y", x.shape, x.dtype, dev), _want(state_out, "state_out", st, x.dtype, dev),
-         _choice(ACTIVATIONS, activation, "activation"), B, C, W, dt)
+    rc = (_bind or _load_bind()).conv_step(x, w, bias, state_in, y, state_in if state_out is None else state_out,
+                                           _choice(ACTIVATIONS, activation, "activation"), _handle(stream))
+    if rc:
+        raise LAError(rc, "la_short_conv_step")
 
 
 def la_short_conv_bwd(x, w, dy, dx, dw, bias=None, dbias=None, state_in=None, dstate_in=None, dstate_out=None,
                       lengths=None, activation: str = "silu", workspace=None, stream=None):
     """dx, dw (and dbias, dstate_out) <- gradients of sum(y * dy) + sum(state_out * dstate_in) for
     la_short_conv_fwd; dstate_out is the gradient of state_in."""
-    import torch
-    dev, dt = _cuda(x, "x", 3)
-    B, T, C = x.shape
-    W = w.shape[-1]
-    st, f32 = (B, W - 1, C), torch.float32
-    wp, wn, _keep = _mixer_workspace("short_conv_bwd", B, T, C, 1, W, dt, workspace, dev, stream)
-    _run("la_short_conv_bwd", dev, stream, x.data_ptr(), _want(w, "w", (C, W), f32, dev),
-         _want(bias, "bias", (C,), f32, dev), _want(state_in, "state_in", st, x.dtype, dev),
-         _want(dy, "dy", x.shape, x.dtype, dev), _want(dstate_in, "dstate_in", st, x.dtype, dev),
-         _want(dx, "dx", x.shape, x.dtype, dev), _want(dw, "dw", (C, W), f32, dev),
-         _want(dbias, "dbias", (C,), f32, dev), _want(dstate_out, "dstate_out", st, x.dtype, dev),
-         _want(lengths, "lengths", (B,), torch.int32, dev), _choice(ACTIVATIONS, activation, "activation"), B, T, C,
-         W, dt, wp, wn)
-
-
-def _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, lead, dev):
-    """Addresses of the scan's inputs and its sizes; lead is (B, T) or (B,)."""
-    import torch
-    C, f32 = x.shape[-1], torch.float32
-    if Bm.dim() != len(lead) + 2:
-        raise ValueError("Bm must be a tensor of %d dimensions ending in [G, N]" % (len(lead) + 2))
-    G, N = Bm.shape[-2:]
-    bc, st = lead + (G, N), (lead[0], C, N)
-    ptrs = (x.data_ptr(), _want(dt, "dt", x.shape, x.dtype, dev), _want(A, "A", (C, N), f32, dev),
-            _want(Bm, "Bm", bc, x.dtype, dev), _want(Cm, "Cm", bc, x.dtype, dev), _want(D, "D", (C,), f32, dev),
-            _want(z, "z", x.shape, x.dtype, dev), _want(dt_bias, "dt_bias", (C,), f32, dev),
-            _want(state_in, "state_in", st, f32, dev))
-    return ptrs, C, G, N, bc, st
+    rc = (_bind or _load_bind()).conv_bwd(x, w, bias, state_in, dy, dstate_in, dx, dw, dbias, dstate_out, lengths,
+                                          _choice(ACTIVATIONS, activation, "activation"), workspace, _handle(stream))
+    if rc:
+        raise LAError(rc, "la_short_conv_bwd")
 
 
 def la_selective_scan_fwd(x, dt, A, Bm, Cm, y, D=None, z=None, dt_bias=None, state_in=None, state_out=None,
                           lengths=None, softplus: bool = True, workspace=None, stream=None):
     """y <- the selective state space scan of x [B, T, C] with steps dt [B, T, C], rates A [C, N] and projections
     Bm, Cm [B, T, G, N]; states [B, C, N] float32 (state_out may be state_in).  See include/la.h."""
-    import torch
-    dev, code = _cuda(x, "x", 3)
-    B, T = x.shape[:2]
-    ptrs, C, G, N, _, st = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, (B, T), dev)
-    wp, wn, _keep = _mixer_workspace("selective_scan_fwd", B, T, C, G, N, code, workspace, dev, stream)
-    _run("la_selective_scan_fwd", dev, stream, *ptrs, _want(y, "y", x.shape, x.dtype, dev),
-         _want(state_out, "state_out", st, torch.float32, dev), _want(lengths, "lengths", (B,), torch.int32, dev),
-         1 if softplus else 0, B, T, C, G, N, code, wp, wn)
+    rc = (_bind or _load_bind()).scan_fwd(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, y, state_out, lengths, softplus,
+                                          workspace, _handle(stream))
+    if rc:
+        raise LAError(rc, "la_selective_scan_fwd")
 
 
 def la_selective_scan_step(x, dt, A, Bm, Cm, y, state_in, state_out=None, D=None, z=None, dt_bias=None,
                            softplus: bool = True, stream=None):
     """One token: x, dt, z, y [B, C], Bm, Cm [B, G, N]; state_out defaults to state_in (updated in place)."""
-    import torch
-    dev, code = _cuda(x, "x", 2)
-    B = x.shape[0]
-    ptrs, C, G, N, _, st = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, (B,), dev)
-    out = ptrs[-1] if state_out is None else _want(state_out, "state_out", st, torch.float32, dev)
-    _run("la_selective_scan_step", dev, stream, *ptrs, _want(y, "y", x.shape, x.dtype, dev), out,
-         1 if softplus else 0, B, C, G, N, code)
+    rc = (_bind or _load_bind()).scan_step(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, y,
+                                           state_in if state_out is None else state_out, softplus, _handle(stream))
+    if rc:
+        raise LAError(rc, "la_selective_scan_step")
 
 
 def la_selective_scan_bwd(x, dt, A, Bm, Cm, dy, dx, ddt, dA, dBm, dCm, D=None, dD=None, z=None, dz=None, dt_bias=None,
@@ -720,49 +627,31 @@ def la_selective_scan_bwd(x, dt, A, Bm, Cm, dy, dx, ddt, dA, dBm, dCm, D=None, d
                           softplus: bool = True, workspace=None, stream=None):
     """Gradients of sum(y * dy) + sum(state_out * dstate_in) for la_selective_scan_fwd; dstate_out is the gradient
     of state_in.  dA, dD, ddt_bias and the states' gradients are float32."""
-    import torch
-    dev, code = _cuda(x, "x", 3)
-    B, T = x.shape[:2]
-    ptrs, C, G, N, bc, st = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, (B, T), dev)
-    f32 = torch.float32
-    wp, wn, _keep = _mixer_workspace("selective_scan_bwd", B, T, C, G, N, code, workspace, dev, stream)
-    _run("la_selective_scan_bwd", dev, stream, *ptrs, _want(dy, "dy", x.shape, x.dtype, dev),
-         _want(dstate_in, "dstate_in", st, f32, dev), _want(dx, "dx", x.shape, x.dtype, dev),
-         _want(ddt, "ddt", x.shape, x.dtype, dev), _want(dA, "dA", (C, N), f32, dev),
-         _want(dBm, "dBm", bc, x.dtype, dev), _want(dCm, "dCm", bc, x.dtype, dev), _want(dD, "dD", (C,), f32, dev),
-         _want(dz, "dz", x.shape, x.dtype, dev), _want(ddt_bias, "ddt_bias", (C,), f32, dev),
-         _want(dstate_out, "dstate_out", st, f32, dev), _want(lengths, "lengths", (B,), torch.int32, dev),
-         1 if softplus else 0, B, T, C, G, N, code, wp, wn)
+    rc = (_bind or _load_bind()).scan_bwd(x, dt, A, Bm, Cm, D, z, dt_bias, state_in, dy, dstate_in, dx, ddt, dA, dBm,
+                                          dCm, dD, dz, ddt_bias, dstate_out, lengths, softplus, workspace,
+                                          _handle(stream))
+    if rc:
+        raise LAError(rc, "la_selective_scan_bwd")
 
 
 def la_group_norm_fwd(x, y, groups: int, gamma=None, beta=None, eps: float = 1e-5, activation: str = "none",
                       mean=None, rstd=None, workspace=None, stream=None):
     """y <- act(gamma * (x - mean) * rstd + beta) for x [B, T, C] with its C channels in `groups` groups; mean and
     rstd [B, groups] float32 receive the statistics that the backward takes.  y may be x."""
-    import torch
-    dev, dt = _cuda(x, "x", 3)
-    B, T, C = x.shape
-    f32, bg = torch.float32, (B, groups)
-    wp, wn, _keep = _mixer_workspace("group_norm_fwd", B, T, C, groups, 1, dt, workspace, dev, stream)
-    _run("la_group_norm_fwd", dev, stream, x.data_ptr(), _want(gamma, "gamma", (C,), f32, dev),
-         _want(beta, "beta", (C,), f32, dev), _want(y, "y", x.shape, x.dtype, dev), _want(mean, "mean", bg, f32, dev),
-         _want(rstd, "rstd", bg, f32, dev), eps, _choice(ACTIVATIONS, activation, "activation"), B, T, C, groups, dt,
-         wp, wn)
+    rc = (_bind or _load_bind()).norm_fwd(x, y, groups, gamma, beta, eps,
+                                          _choice(ACTIVATIONS, activation, "activation"), mean, rstd, workspace,
+                                          _handle(stream))
+    if rc:
+        raise LAError(rc, "la_group_norm_fwd")
 
 
 def la_group_norm_bwd(x, dy, dx, groups: int, mean, rstd, gamma=None, beta=None, dgamma=None, dbeta=None,
                       activation: str = "none", workspace=None, stream=None):
     """dx (may be dy), dgamma, dbeta <- gradients of sum(y * dy) for la_group_norm_fwd."""
-    import torch
-    dev, dt = _cuda(x, "x", 3)
-    B, T, C = x.shape
-    f32, bg = torch.float32, (B, groups)
-    wp, wn, _keep = _mixer_workspace("group_norm_bwd", B, T, C, groups, 1, dt, workspace, dev, stream)
-    _run("la_group_norm_bwd", dev, stream, x.data_ptr(), _want(dy, "dy", x.shape, x.dtype, dev),
-         _want(mean, "mean", bg, f32, dev), _want(rstd, "rstd", bg, f32, dev), _want(gamma, "gamma", (C,), f32, dev),
-         _want(beta, "beta", (C,), f32, dev), _want(dx, "dx", x.shape, x.dtype, dev),
-         _want(dgamma, "dgamma", (C,), f32, dev), _want(dbeta, "dbeta", (C,), f32, dev),
-         _choice(ACTIVATIONS, activation, "activation"), B, T, C, groups, dt, wp, wn)
+    rc = (_bind or _load_bind()).norm_bwd(x, dy, dx, groups, mean, rstd, gamma, beta, dgamma, dbeta,
+                                          _choice(ACTIVATIONS, activation, "activation"), workspace, _handle(stream))
+    if rc:
+        raise LAError(rc, "la_group_norm_bwd")
 
 
 def la_status_string(status: int) -> str:

@@ -2,7 +2,8 @@
 
 Run ``python -m linear_attention_attn_b200.build`` (or call ``build()``).  Each
 .cu file is compiled separately (in parallel) and linked with the static CUDA
-runtime; no GPU is needed.  The driver API entry point used for TMA
+runtime; no GPU is needed.  csrc/la_bind.cpp, the module that hands torch tensors
+to the library's entry points, is compiled with g++ against torch's headers.  The driver API entry point used for TMA
 descriptors is resolved at run time, so nothing links against libcuda.
 """
 from __future__ import annotations
@@ -18,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libla_b200.so")
+BIND_SRC = os.path.join(CSRC, "la_bind.cpp")
+BIND = os.path.join(PKG, "_la_bind.so")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -53,6 +56,36 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_bind(force: bool) -> str:
+    obj = os.path.join(OBJ, "la_bind.o")
+    newest = max(os.path.getmtime(BIND_SRC), _newest(glob.glob(os.path.join(INCLUDE, "*.h"))))
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest:
+        return obj
+    import sysconfig
+    from importlib.util import find_spec
+    torch_inc = os.path.join(os.path.dirname(find_spec("torch").origin), "include")
+    cuda_inc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE]
+    for d in (torch_inc, os.path.join(torch_inc, "torch", "csrc", "api", "include"), cuda_inc):
+        cmd += ["-isystem", d]
+    r = subprocess.run(cmd + ["-c", BIND_SRC, "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s%s" % (BIND_SRC, r.stdout, r.stderr))
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    from importlib.util import find_spec
+    torch_lib = os.path.join(os.path.dirname(find_spec("torch").origin), "lib")
+    tmp = BIND + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libla_b200.so", "-Wl,-rpath,$ORIGIN", "-L" + torch_lib,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if anything changed) and return the path of libla_b200.so."""
     os.makedirs(OBJ, exist_ok=True)
@@ -60,7 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force:
         for o in glob.glob(os.path.join(OBJ, "*.o")):
             os.remove(o)
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        bind = ex.submit(_compile_bind, force)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
         tmp = LIB + ".tmp%d" % os.getpid()
@@ -69,6 +103,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
         os.replace(tmp, LIB)
+    obj = bind.result()
+    if force or not os.path.exists(BIND) or os.path.getmtime(BIND) < os.path.getmtime(obj):
+        _link_bind(obj)
     return LIB
 
 
