@@ -23,9 +23,72 @@ __device__ __forceinline__ int seq_end(const int *lengths, int b, int T) {
     return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
+// The taps of V channels, w[c .. c + V)[W]: V W neighbouring floats, read 16 bytes at a time where
+// the array is aligned to them; and their biases.
+template <int V, int W>
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, Lanes<V> (&w)[W], Lanes<V> &bias) {
+    const float *p = a.w + (long long)c * W;
+    float f[V * W], v[V];
+    if ((V * W) % 4 == 0 && ((uintptr_t)a.w & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < V * W / 4; ++i) {
+            const float4 q = reinterpret_cast<const float4 *>(p)[i];
+            f[4 * i] = q.x; f[4 * i + 1] = q.y; f[4 * i + 2] = q.z; f[4 * i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; ++i) f[i] = p[i];
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = f[i * W + j];
+        w[j].set(v);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = a.bias ? a.bias[c + i] : 0.f;
+    bias.set(v);
+}
+
+// The W - 1 inputs before token t0: from x, from the entering state, or zeros.
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_window(const T *x, const T *first, int t0, int n, long long C,
+                                            Lanes<V> (&win)[W - 1]) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int u = t0 - (W - 1) + j;
+        Raw<T, V> r;
+        r.load(u >= 0 ? x + u * C : first + (u + W - 1) * C, u >= 0 ? u < n : first != nullptr);
+        win[j] = r.lanes();
+    }
+}
+
+// s = bias + sum_j w[j] x[t-W+1+j], the window's inputs and the current one.
+template <int V, int W>
+__device__ __forceinline__ Lanes<V> convolve(const Lanes<V> (&w)[W], const Lanes<V> &bias, const Lanes<V> (&win)[W - 1],
+                                             const Lanes<V> &cur) {
+    Lanes<V> s = bias;
+#pragma unroll
+    for (int i = 0; i < Lanes<V>::n; ++i) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) s.e[i] = fma(w[j].e[i], win[j].e[i], s.e[i]);
+        s.e[i] = fma(w[W - 1].e[i], cur.e[i], s.e[i]);
+    }
+    return s;
+}
+
+template <int V, int N>
+__device__ __forceinline__ void shift(Lanes<V> (&win)[N], const Lanes<V> &cur) {
+#pragma unroll
+    for (int j = 0; j + 1 < N; ++j) win[j] = win[j + 1];
+    win[N - 1] = cur;
+}
+
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads)
 conv_fwd_kernel(ConvArgs a, int cvecs, int segs) {
+    typedef Lanes<V> L;
+    constexpr int U = V == 8 ? 4 : 8;          // rows in flight
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (idx >= (long long)a.B * segs * cvecs) return;
     const long long bs = idx / cvecs;
@@ -34,81 +97,125 @@ conv_fwd_kernel(ConvArgs a, int cvecs, int segs) {
     const int n = seq_end(a.lengths, b, a.T);
     const int t0 = seg * kSeg, t1 = min(t0 + kSeg, a.T);
     const long long C = a.C;
-    const T *x = (const T *)a.x + (long long)b * a.T * C + c;
-    T *y = (T *)a.y + (long long)b * a.T * C + c;
+    const T *__restrict__ x = (const T *)a.x + (long long)b * a.T * C + c;
+    T *__restrict__ y = (T *)a.y + (long long)b * a.T * C + c;
     const T *first = a.state_in ? (const T *)a.state_in + (long long)b * (W - 1) * C + c : nullptr;
 
-    float w[W][V], bias[V], win[W - 1][V];
+    Raw<T, V> row[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        bias[i] = a.bias ? a.bias[c + i] : 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = a.w[(long long)(c + i) * W + j];
-    }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int u = t0 - (W - 1) + j;
-#pragma unroll
-        for (int i = 0; i < V; ++i) win[j][i] = 0.f;
-        if (u >= 0) {
-            if (u < n) ldv<V>(x + u * C, win[j]);
-        } else if (first) {
-            ldv<V>(first + (u + W - 1) * C, win[j]);
-        }
-    }
+    for (int u = 0; u < U; ++u) row[u].load(x + (t0 + u) * C, t0 + u < n);
+    L w[W], bias, win[W - 1];
+    load_taps<V, W>(a, c, w, bias);
+    load_window<T, V, W>(x, first, t0, n, C, win);
     // The state after n tokens: rows n .. n + W - 2 of the sequence extended by the entering state.  It
     // leaves through the only thread that reads the entering one, so the two may be one buffer.
     if (seg == 0 && a.state_out) {
-        Pack<T, V> keep[W - 1];
+        Raw<T, V> keep[W - 1];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int r = n + j;
-            if (r >= W - 1) {
-                keep[j] = *reinterpret_cast<const Pack<T, V> *>(x + (r - (W - 1)) * C);
-            } else if (first) {
-                keep[j] = *reinterpret_cast<const Pack<T, V> *>(first + r * C);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) keep[j].v[i] = from_f<T>(0.f);
-            }
+            keep[j].load(r >= W - 1 ? x + (r - (W - 1)) * C : first + r * C, r >= W - 1 || first);
         }
         T *so = (T *)a.state_out + (long long)b * (W - 1) * C + c;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Pack<T, V> *>(so + j * C) = keep[j];
+        for (int j = 0; j < W - 1; ++j) keep[j].store(so + j * C);
     }
-#pragma unroll 4
-    for (int t = t0; t < t1; ++t) {
-        float cur[V], o[V];
-        if (t < n) {
-            ldv<V>(x + t * C, cur);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float s = bias[i];
+    for (int h = 0; h < kSeg; h += U) {
+        const int tb = t0 + h;
+        if (tb >= t1) break;
+        Raw<T, V> next[U];
+        if (h + U < kSeg)
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
-                s = fmaf(w[W - 1][i], cur[i], s);
-                o[i] = a.silu ? s * sigmoid_f(s) : s;
+            for (int u = 0; u < U; ++u) next[u].load(x + (tb + U + u) * C, tb + U + u < n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = tb + u;
+            const L cur = row[u].lanes();
+            L o = convolve<V, W>(w, bias, win, cur);
+#pragma unroll
+            for (int i = 0; i < L::n; ++i) {
+                if (a.silu) o.e[i] = mul(o.e[i], sigmoid(o.e[i]));
+                if (t >= n) o.e[i] = L::splat(0.f);
             }
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
-#pragma unroll
-            for (int i = 0; i < V; ++i) win[W - 2][i] = cur[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = 0.f;
+            if (t < t1) store_lanes<V>(y + t * C, o);
+            shift<V, W - 1>(win, cur);
         }
-        stv<V>(y + t * C, o);
+        if (h + U < kSeg)
+#pragma unroll
+            for (int u = 0; u < U; ++u) row[u] = next[u];
     }
 }
 
 // Backward.  Block: 32 channel vectors x kBwdSegs segments of `seg` tokens of one batch entry.
 constexpr int kBwdSegs = 8;
 
+// U tokens from tb on.  Inner: all of them lie in the segment and the sequence, and so do the
+// W - 1 tokens before them.
+template <typename T, int V, int W, int U, bool INNER>
+__device__ __forceinline__ void bwd_tokens(const ConvArgs &a, const Raw<T, V> (&rx)[U], const Raw<T, V> (&rg)[U],
+                                           const Lanes<V> (&w)[W], const Lanes<V> &bias, Lanes<V> (&win)[W - 1],
+                                           Lanes<V> (&gw)[W - 1], Lanes<V> (&dw)[W], Lanes<V> &db, int tb, int t0,
+                                           int t1, int n, T *__restrict__ dx, T *dfirst, const T *ds) {
+    typedef Lanes<V> L;
+    const long long C = a.C;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int t = tb + k;
+        const L cur = rx[k].lanes();
+        L g = rg[k].lanes();
+        if (a.silu) {
+            const L s = convolve<V, W>(w, bias, win, cur);
+#pragma unroll
+            for (int i = 0; i < L::n; ++i) {
+                // sg (1 + s (1 - sg))
+                const auto sg = sigmoid(s.e[i]), r = fma(sg, L::splat(-1.f), L::splat(1.f));
+                g.e[i] = mul(mul(g.e[i], sg), fma(s.e[i], r, L::splat(1.f)));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < L::n; ++i) {
+            if (!INNER && t >= n) g.e[i] = L::splat(0.f);
+            if (INNER || t < t1) {
+                db.e[i] = add(db.e[i], g.e[i]);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) dw[j].e[i] = fma(g.e[i], win[j].e[i], dw[j].e[i]);
+                dw[W - 1].e[i] = fma(g.e[i], cur.e[i], dw[W - 1].e[i]);
+            }
+        }
+        const int u = t - (W - 1);
+        if (INNER || (u < t1 && (u >= t0 || (t0 == 0 && dfirst)))) {
+            // dx[u] = sum_k w[W-1-k] g[u+k]: g[u] is the oldest in the window
+            L d;
+#pragma unroll
+            for (int i = 0; i < L::n; ++i) {
+                d.e[i] = mul(w[0].e[i], g.e[i]);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) d.e[i] = fma(w[W - 1 - j].e[i], gw[j].e[i], d.e[i]);
+            }
+            if (INNER) {
+                store_lanes<V>(dx + u * C, d);
+            } else {
+                const int j = u + (W - 1) - n;          // u's row of the leaving state
+                if (ds && u < n && j >= 0) {
+                    Raw<T, V> e;
+                    e.load(ds + j * C);
+                    const L el = e.lanes();
+#pragma unroll
+                    for (int i = 0; i < L::n; ++i) d.e[i] = add(d.e[i], el.e[i]);
+                }
+                store_lanes<V>(u >= 0 ? dx + u * C : dfirst + (u + W - 1) * C, d);
+            }
+        }
+        shift<V, W - 1>(win, cur);
+        shift<V, W - 1>(gw, g);
+    }
+}
+
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * kBwdSegs)
+__global__ void __launch_bounds__(32 * kBwdSegs, W <= 4 ? 2 : 1)
 conv_bwd_kernel(ConvArgs a, int seg, int blocks_t, int blocks_c, float *part) {
+    typedef Lanes<V> L;
     __shared__ float red[kBwdSegs][32 * V * (W + 1) + 1];
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int p = blockIdx.x / blocks_c, bc = blockIdx.x - p * blocks_c;   // token block, channel block
@@ -116,109 +223,64 @@ conv_bwd_kernel(ConvArgs a, int seg, int blocks_t, int blocks_c, float *part) {
     const int b = p / blocks_t, bt = p - b * blocks_t;
     const long long C = a.C;
     const bool live = c < a.C;
-    float dw[W][V], db[V];
+    L dw[W], db;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < L::n; ++i) {
+        db.e[i] = L::splat(0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j].e[i] = L::splat(0.f);
     }
     const long long t0l = ((long long)bt * kBwdSegs + row) * seg;
     if (live && t0l < a.T) {
+        constexpr int U = 4;                   // rows in flight, of x and of dy
         const int t0 = (int)t0l, t1 = (int)min((long long)a.T, t0l + seg);
-        const int n = seq_end(a.lengths, b, a.T);
-        const T *x = (const T *)a.x + (long long)b * a.T * C + c;
-        const T *dy = (const T *)a.dy + (long long)b * a.T * C + c;
-        T *dx = (T *)a.dx + (long long)b * a.T * C + c;
+        const int n = seq_end(a.lengths, b, a.T), end = t1 + W - 1, have = min(n, end);
+        const T *__restrict__ x = (const T *)a.x + (long long)b * a.T * C + c;
+        const T *__restrict__ dy = (const T *)a.dy + (long long)b * a.T * C + c;
+        T *__restrict__ dx = (T *)a.dx + (long long)b * a.T * C + c;
         const T *first = a.state_in ? (const T *)a.state_in + (long long)b * (W - 1) * C + c : nullptr;
         const T *ds = a.dstate_in ? (const T *)a.dstate_in + (long long)b * (W - 1) * C + c : nullptr;
         T *dfirst = a.dstate_out ? (T *)a.dstate_out + (long long)b * (W - 1) * C + c : nullptr;
-        float w[W][V], bias[V], win[W - 1][V], gw[W - 1][V];
+        Raw<T, V> rx[U], rg[U];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            bias[i] = a.bias ? a.bias[c + i] : 0.f;
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = a.w[(long long)(c + i) * W + j];
+        for (int k = 0; k < U; ++k) {
+            rx[k].load(x + (t0 + k) * C, t0 + k < have);
+            rg[k].load(dy + (t0 + k) * C, t0 + k < have);
         }
+        L w[W], bias, win[W - 1], gw[W - 1];
+        load_taps<V, W>(a, c, w, bias);
+        load_window<T, V, W>(x, first, t0, n, C, win);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            const int u = t0 - (W - 1) + j;
+        for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) { win[j][i] = 0.f; gw[j][i] = 0.f; }
-            if (u >= 0) {
-                if (u < n) ldv<V>(x + u * C, win[j]);
-            } else if (first) {
-                ldv<V>(first + (u + W - 1) * C, win[j]);
-            }
-        }
+            for (int i = 0; i < L::n; ++i) gw[j].e[i] = L::splat(0.f);
         // at step t: g[t] is formed, and dx[u] with u = t - (W - 1) is complete
-#pragma unroll 2
-        for (int t = t0; t < t1 + W - 1; ++t) {
-            float cur[V], g[V];
+        for (int tb = t0; tb < end; tb += U) {
+            Raw<T, V> nx[U], ng[U];
 #pragma unroll
-            for (int i = 0; i < V; ++i) { cur[i] = 0.f; g[i] = 0.f; }
-            if (t < n) {
-                ldv<V>(x + t * C, cur);
-                ldv<V>(dy + t * C, g);
-                if (a.silu) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float s = bias[i];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
-                        s = fmaf(w[W - 1][i], cur[i], s);
-                        const float sg = sigmoid_f(s);
-                        g[i] *= sg * fmaf(s, 1.f - sg, 1.f);
-                    }
-                }
-                if (t < t1) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        db[i] += g[i];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(g[i], win[j][i], dw[j][i]);
-                        dw[W - 1][i] = fmaf(g[i], cur[i], dw[W - 1][i]);
-                    }
-                }
+            for (int k = 0; k < U; ++k) {
+                nx[k].load(x + (tb + U + k) * C, tb + U + k < have);
+                ng[k].load(dy + (tb + U + k) * C, tb + U + k < have);
             }
-            const int u = t - (W - 1);
-            if (u >= t0 || (t0 == 0 && dfirst)) {
-                // dx[u] = sum_k w[W-1-k] g[u+k]: g[u] is the oldest in the window
-                float d[V];
+            if (tb - (W - 1) >= t0 && tb + U <= min(t1, n))
+                bwd_tokens<T, V, W, U, true>(a, rx, rg, w, bias, win, gw, dw, db, tb, t0, t1, n, dx, dfirst, ds);
+            else
+                bwd_tokens<T, V, W, U, false>(a, rx, rg, w, bias, win, gw, dw, db, tb, t0, t1, n, dx, dfirst, ds);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    d[i] = w[0][i] * g[i];
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k) d[i] = fmaf(w[W - 1 - k][i], gw[k][i], d[i]);
-                }
-                const int j = u + (W - 1) - n;          // u's row of the leaving state
-                if (ds && u < n && j >= 0) {
-                    float e[V];
-                    ldv<V>(ds + j * C, e);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) d[i] += e[i];
-                }
-                stv<V>(u >= 0 ? dx + u * C : dfirst + (u + W - 1) * C, d);
-            }
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    win[j][i] = win[j + 1][i];
-                    gw[j][i] = gw[j + 1][i];
-                }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                win[W - 2][i] = cur[i];
-                gw[W - 2][i] = g[i];
+            for (int k = 0; k < U; ++k) {
+                rx[k] = nx[k];
+                rg[k] = ng[k];
             }
         }
     }
+    {
+        float v[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int j = 0; j <= W; ++j) {
+            (j < W ? dw[j] : db).get(v);
 #pragma unroll
-        for (int j = 0; j < W; ++j) red[row][(lane * V + i) * (W + 1) + j] = dw[j][i];
-        red[row][(lane * V + i) * (W + 1) + W] = db[i];
+            for (int i = 0; i < V; ++i) red[row][(lane * V + i) * (W + 1) + j] = v[i];
+        }
     }
     __syncthreads();
     const int n_out = min(32 * V, a.C - bc * 32 * V) * (W + 1);

@@ -47,10 +47,129 @@ inline int vec_width(size_t elem, long long unit, uintptr_t address_bits) {
 inline size_t elem_bytes(la_dtype dt) { return dt == LA_F32 ? 4 : 2; }
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// -------------------------------------------------- packed fp32 arithmetic --
+// Two fp32 operations at once on a register pair.  Kernels that work on V neighbouring channels
+// hold them as Lanes<V>: V / 2 pairs, or one float.
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two fp32 operations at once on a register pair.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(ex2(a), ex2(b));
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ f2 both(float x) { return pack2(x, x); }
+
+// The same operations by element type, float or pair.
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ f2 mul(f2 a, f2 b) { return mul2(a, b); }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ f2 add(f2 a, f2 b) { return add2(a, b); }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
+
 // ----------------------------------------------------------- activations --
 // 1 / (1 + e^-x).  For x below about -88 the exponential overflows to infinity and the result
-// is 0; the relative error is that of the fast exponential, a few 2^-22 where |x| is a few units.
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// is 0; the relative error is a few 2^-22 where |x| is a few units.
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+    float a, b;
+    unpack2(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
+    return pack2(rcp(a), rcp(b));
+}
+
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
+__device__ __forceinline__ float sigmoid(float x) { return sigmoid_f(x); }
+__device__ __forceinline__ f2 sigmoid(f2 x) { return sigmoid2(x); }
+
+template <int V> struct Lanes {
+    typedef f2 E;
+    static constexpr int n = V / 2;
+    E e[n];
+    static __device__ __forceinline__ E splat(float x) { return both(x); }
+    __device__ __forceinline__ void set(const float (&v)[V]) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) e[i] = pack2(v[2 * i], v[2 * i + 1]);
+    }
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+        for (int i = 0; i < n; ++i) unpack2(e[i], v[2 * i], v[2 * i + 1]);
+    }
+};
+template <> struct Lanes<1> {
+    typedef float E;
+    static constexpr int n = 1;
+    E e[1];
+    static __device__ __forceinline__ E splat(float x) { return x; }
+    __device__ __forceinline__ void set(const float (&v)[1]) { e[0] = v[0]; }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = e[0]; }
+};
+
+// V elements as they lie in memory, in whole words: a load that may be left out (zeros then) is not
+// waited for before its values are used, as it would be if its elements were taken apart at once.
+template <int BYTES> struct WordsOf;
+template <> struct WordsOf<2> { typedef unsigned short W; static __device__ __forceinline__ W zero() { return 0; } };
+template <> struct WordsOf<4> { typedef unsigned W; static __device__ __forceinline__ W zero() { return 0; } };
+template <> struct WordsOf<8> { typedef uint2 W; static __device__ __forceinline__ W zero() { return make_uint2(0, 0); } };
+template <> struct WordsOf<16> { typedef uint4 W; static __device__ __forceinline__ W zero() { return make_uint4(0, 0, 0, 0); } };
+template <typename T, int V> struct Raw {
+    typedef WordsOf<sizeof(T) * V> O;
+    typename O::W w;
+    __device__ __forceinline__ void load(const T *p, bool there = true) {
+        w = O::zero();
+        if (there) w = *reinterpret_cast<const typename O::W *>(p);
+    }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<typename O::W *>(p) = w; }
+    __device__ __forceinline__ Lanes<V> lanes() const {
+        Pack<T, V> k;
+        *reinterpret_cast<typename O::W *>(&k) = w;
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = to_f(k.v[i]);
+        Lanes<V> r;
+        r.set(v);
+        return r;
+    }
+};
+template <int V, typename T>
+__device__ __forceinline__ void store_lanes(T *p, const Lanes<V> &x) {
+    float v[V];
+    x.get(v);
+    stv<V>(p, v);
+}
 
 // --------------------------------------------------- internal entry points --
 struct RotaryArgs {

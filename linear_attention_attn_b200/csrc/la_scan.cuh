@@ -12,49 +12,6 @@ namespace scan {
 
 constexpr int kNS = 4;             // states a lane holds
 constexpr int kTile = 16;          // tokens staged in shared memory at a time
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two fp32 operations at once on a register pair.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 ex2_2(f2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    return pack2(ex2(a), ex2(b));
-}
-
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ f2 both(float x) { return pack2(x, x); }
 
 // e^-|r| of a pair (0 from 128 on) with the argument's rounding repaired: r log2(e) as a product
 // and its remainder, and the part of log2(e) that one float leaves out.
@@ -90,13 +47,6 @@ __device__ __forceinline__ float softplus_f(float r) {
     unpack2(softplus2(both(r)), a, b);
     return a;
 }
-// 1 / (1 + e^-x) of a pair.
-__device__ __forceinline__ f2 sigmoid2(f2 x) {
-    float a, b;
-    unpack2(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
-    return pack2(rcp(a), rcp(b));
-}
-
 __device__ __forceinline__ int seq_end(const int *lengths, int b, int T) {
     return lengths ? min(max(lengths[b], 0), T) : T;
 }
