@@ -149,6 +149,7 @@ conv_fwd_kernel(ConvArgs a, int cvecs, int segs) {
 
 // Backward.  Block: 32 channel vectors x kBwdSegs segments of `seg` tokens of one batch entry.
 constexpr int kBwdSegs = 8;
+constexpr int kBwdRows = 4;        // rows taken at a time
 
 // U tokens from tb on.  Inner: all of them lie in the segment and the sequence, and so do the
 // W - 1 tokens before them.
@@ -212,11 +213,84 @@ __device__ __forceinline__ void bwd_tokens(const ConvArgs &a, const Raw<T, V> (&
     }
 }
 
+// Rows of x and dy on their way to a thread, U at a time.  Where an access has at least 4 bytes they
+// come through the thread's own places in shared memory by asynchronous copies, 2 to 4 groups ahead,
+// so that no registers hold them; 2-byte accesses go to registers, one group ahead.
+template <typename T, int V, int U, bool ASYNC = (sizeof(T) * V >= 4)> struct Feed;
+template <typename T, int V, int U> struct Feed<T, V, U, true> {
+    typedef typename WordsOf<sizeof(T) * V>::W Word;
+    static constexpr int kAhead = sizeof(Word) == 16 ? 2 : 4;          // at most 64 KB a block: three blocks an SM
+    static constexpr size_t bytes = sizeof(Word) * kAhead * U * 2 * 32 * kBwdSegs;
+    Word *s;
+    const T *x, *g;
+    int t, have, slot;
+    long long C;
+    __device__ __forceinline__ Feed(void *smem, const T *x_, const T *g_, int t0, int have_, long long C_)
+        : s((Word *)smem + threadIdx.x), x(x_ + t0 * C_), g(g_ + t0 * C_), t(t0), have(have_), slot(0), C(C_) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) put(i);
+    }
+    __device__ __forceinline__ Word *at(int place, int k, int which) {
+        return s + ((place * U + k) * 2 + which) * (32 * kBwdSegs);
+    }
+    __device__ __forceinline__ void put(int place) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            copy_async<sizeof(Word)>(at(place, k, 0), x + k * C, t + k < have);
+            copy_async<sizeof(Word)>(at(place, k, 1), g + k * C, t + k < have);
+        }
+        copy_commit();
+        x += U * C;
+        g += U * C;
+        t += U;
+    }
+    __device__ __forceinline__ void take(Raw<T, V> (&rx)[U], Raw<T, V> (&rg)[U]) {
+        copy_wait<kAhead - 1>();
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            rx[k].w = *at(slot, k, 0);
+            rg[k].w = *at(slot, k, 1);
+        }
+        put(slot);
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
+    }
+};
+template <typename T, int V, int U> struct Feed<T, V, U, false> {
+    static constexpr size_t bytes = 0;
+    Raw<T, V> nx[U], ng[U];
+    const T *x, *g;
+    int t, have;
+    long long C;
+    __device__ __forceinline__ Feed(void *, const T *x_, const T *g_, int t0, int have_, long long C_)
+        : x(x_ + t0 * C_), g(g_ + t0 * C_), t(t0), have(have_), C(C_) { put(); }
+    __device__ __forceinline__ void put() {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            nx[k].load(x + k * C, t + k < have);
+            ng[k].load(g + k * C, t + k < have);
+        }
+        x += U * C;
+        g += U * C;
+        t += U;
+    }
+    __device__ __forceinline__ void take(Raw<T, V> (&rx)[U], Raw<T, V> (&rg)[U]) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            rx[k] = nx[k];
+            rg[k] = ng[k];
+        }
+        put();
+    }
+};
+
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(32 * kBwdSegs, W <= 4 ? 2 : 1)
 conv_bwd_kernel(ConvArgs a, int seg, int blocks_t, int blocks_c, float *part) {
     typedef Lanes<V> L;
-    __shared__ float red[kBwdSegs][32 * V * (W + 1) + 1];
+    // the rows on their way, and after them the segments' sums [kBwdSegs][kRed]
+    extern __shared__ uint4 s_feed[];
+    constexpr int kRed = 32 * V * (W + 1) + 1;
+    float *red = reinterpret_cast<float *>(s_feed);
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int p = blockIdx.x / blocks_c, bc = blockIdx.x - p * blocks_c;   // token block, channel block
     const int c = (bc * 32 + lane) * V;
@@ -232,7 +306,7 @@ conv_bwd_kernel(ConvArgs a, int seg, int blocks_t, int blocks_c, float *part) {
     }
     const long long t0l = ((long long)bt * kBwdSegs + row) * seg;
     if (live && t0l < a.T) {
-        constexpr int U = 4;                   // rows in flight, of x and of dy
+        constexpr int U = kBwdRows;
         const int t0 = (int)t0l, t1 = (int)min((long long)a.T, t0l + seg);
         const int n = seq_end(a.lengths, b, a.T), end = t1 + W - 1, have = min(n, end);
         const T *__restrict__ x = (const T *)a.x + (long long)b * a.T * C + c;
@@ -241,12 +315,7 @@ conv_bwd_kernel(ConvArgs a, int seg, int blocks_t, int blocks_c, float *part) {
         const T *first = a.state_in ? (const T *)a.state_in + (long long)b * (W - 1) * C + c : nullptr;
         const T *ds = a.dstate_in ? (const T *)a.dstate_in + (long long)b * (W - 1) * C + c : nullptr;
         T *dfirst = a.dstate_out ? (T *)a.dstate_out + (long long)b * (W - 1) * C + c : nullptr;
-        Raw<T, V> rx[U], rg[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            rx[k].load(x + (t0 + k) * C, t0 + k < have);
-            rg[k].load(dy + (t0 + k) * C, t0 + k < have);
-        }
+        Feed<T, V, U> feed(s_feed, x, dy, t0, have, C);
         L w[W], bias, win[W - 1], gw[W - 1];
         load_taps<V, W>(a, c, w, bias);
         load_window<T, V, W>(x, first, t0, n, C, win);
@@ -256,30 +325,23 @@ conv_bwd_kernel(ConvArgs a, int seg, int blocks_t, int blocks_c, float *part) {
             for (int i = 0; i < L::n; ++i) gw[j].e[i] = L::splat(0.f);
         // at step t: g[t] is formed, and dx[u] with u = t - (W - 1) is complete
         for (int tb = t0; tb < end; tb += U) {
-            Raw<T, V> nx[U], ng[U];
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                nx[k].load(x + (tb + U + k) * C, tb + U + k < have);
-                ng[k].load(dy + (tb + U + k) * C, tb + U + k < have);
-            }
+            Raw<T, V> rx[U], rg[U];
+            feed.take(rx, rg);
             if (tb - (W - 1) >= t0 && tb + U <= min(t1, n))
                 bwd_tokens<T, V, W, U, true>(a, rx, rg, w, bias, win, gw, dw, db, tb, t0, t1, n, dx, dfirst, ds);
             else
                 bwd_tokens<T, V, W, U, false>(a, rx, rg, w, bias, win, gw, dw, db, tb, t0, t1, n, dx, dfirst, ds);
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                rx[k] = nx[k];
-                rg[k] = ng[k];
-            }
         }
+        copy_wait<0>();
     }
+    __syncthreads();
     {
         float v[V];
 #pragma unroll
         for (int j = 0; j <= W; ++j) {
             (j < W ? dw[j] : db).get(v);
 #pragma unroll
-            for (int i = 0; i < V; ++i) red[row][(lane * V + i) * (W + 1) + j] = v[i];
+            for (int i = 0; i < V; ++i) red[row * kRed + (lane * V + i) * (W + 1) + j] = v[i];
         }
     }
     __syncthreads();
@@ -287,7 +349,7 @@ conv_bwd_kernel(ConvArgs a, int seg, int blocks_t, int blocks_c, float *part) {
     for (int e = threadIdx.x; e < n_out; e += 32 * kBwdSegs) {
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < kBwdSegs; ++r) s += red[r][e];
+        for (int r = 0; r < kBwdSegs; ++r) s += red[r * kRed + e];
         part[((long long)p * a.C + bc * 32 * V) * (W + 1) + e] = s;
     }
 }
@@ -343,8 +405,9 @@ template <typename T, int V, int W>
 la_status bwd_v(const ConvArgs &a, cudaStream_t st) {
     const int seg = bwd_seg(a.B, a.T, a.C), bt = bwd_blocks_t(a.B, a.T, a.C);
     const int bc = (a.C + 32 * V - 1) / (32 * V);
+    const size_t sums = sizeof(float) * kBwdSegs * (32 * V * (W + 1) + 1), feed = Feed<T, V, kBwdRows>::bytes;
     la_status rc = launch("short_conv_bwd", conv_bwd_kernel<T, V, W>, dim3((unsigned)a.B * bt * bc),
-                          dim3(32 * kBwdSegs), 0, st, a, seg, bt, bc, (float *)a.ws);
+                          dim3(32 * kBwdSegs), feed > sums ? feed : sums, st, a, seg, bt, bc, (float *)a.ws);
     if (rc != LA_OK) return rc;
     return launch("short_conv_bwd_reduce", conv_bwd_reduce, dim3((unsigned)((a.C * (W + 1) + 31) / 32)), dim3(256), 0,
                   st, (const float *)a.ws, a.B * bt, a.C, W, a.dw, a.dbias);

@@ -164,6 +164,19 @@ template <typename T, int V> struct Raw {
         return r;
     }
 };
+// An asynchronous copy of BYTES (4, 8 or 16) into the thread's own place in shared memory, zeros
+// where `there` is false (nothing is read then), and the waits on the groups of them.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *smem, const void *p, bool there) {
+    const unsigned d = (unsigned)__cvta_generic_to_shared(smem);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(p), "n"(BYTES), "r"(there ? BYTES : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 template <int V, typename T>
 __device__ __forceinline__ void store_lanes(T *p, const Lanes<V> &x) {
     float v[V];

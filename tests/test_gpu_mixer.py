@@ -109,7 +109,7 @@ def test_rotary_positions_in_place_and_single_tensor():
 
 CONV = [("f32", 2, 37, 64, 4, "silu"), ("f16", 3, 16, 72, 3, "silu"), ("bf16", 2, 300, 130, 4, "silu"),
         ("bf16", 6, 33, 11, 2, "none"), ("f16", 1, 2, 40, 8, "silu"), ("f32", 4, 1, 5, 4, "none"),
-        ("f32", 6, 50, 12, 7, "silu"), ("f16", 2, 700, 64, 5, "none"), ("bf16", 2, 65, 24, 6, "silu")]
+        ("f32", 6, 50, 12, 7, "silu"), ("f16", 2, 700, 64, 5, "none"), ("bf16", 2, 90, 34, 8, "silu"), ("f32", 2, 90, 68, 8, "silu"), ("bf16", 2, 65, 24, 6, "silu")]
 
 
 @pytest.mark.parametrize("dtype,B,T,C,W,act", CONV)
