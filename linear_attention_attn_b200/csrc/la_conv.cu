@@ -101,9 +101,19 @@ conv_fwd_kernel(ConvArgs a, int cvecs, int segs) {
     T *__restrict__ y = (T *)a.y + (long long)b * a.T * C + c;
     const T *first = a.state_in ? (const T *)a.state_in + (long long)b * (W - 1) * C + c : nullptr;
 
+    const int Ci = a.C, live = min(n, t1) - t0;        // rows of the segment that exist
+    const T *__restrict__ px = x + t0 * C;
+    T *__restrict__ py = y + t0 * C;
+    if (live <= 0 && seg > 0) {
+        Lanes<V> zero;
+#pragma unroll
+        for (int i = 0; i < L::n; ++i) zero.e[i] = L::splat(0.f);
+        for (int u = 0; u < t1 - t0; ++u) store_lanes<V>(py + (long long)u * Ci, zero);
+        return;
+    }
     Raw<T, V> row[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) row[u].load(x + (t0 + u) * C, t0 + u < n);
+    for (int u = 0; u < U; ++u) row[u].load(px + (long long)u * Ci, u < live);
     L w[W], bias, win[W - 1];
     load_taps<V, W>(a, c, w, bias);
     load_window<T, V, W>(x, first, t0, n, C, win);
@@ -122,23 +132,21 @@ conv_fwd_kernel(ConvArgs a, int cvecs, int segs) {
     }
 #pragma unroll
     for (int h = 0; h < kSeg; h += U) {
-        const int tb = t0 + h;
-        if (tb >= t1) break;
+        if (t0 + h >= t1) break;
         Raw<T, V> next[U];
         if (h + U < kSeg)
 #pragma unroll
-            for (int u = 0; u < U; ++u) next[u].load(x + (tb + U + u) * C, tb + U + u < n);
+            for (int u = 0; u < U; ++u) next[u].load(px + (long long)(h + U + u) * Ci, h + U + u < live);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = tb + u;
             const L cur = row[u].lanes();
             L o = convolve<V, W>(w, bias, win, cur);
 #pragma unroll
             for (int i = 0; i < L::n; ++i) {
                 if (a.silu) o.e[i] = mul(o.e[i], sigmoid(o.e[i]));
-                if (t >= n) o.e[i] = L::splat(0.f);
+                if (h + u >= live) o.e[i] = L::splat(0.f);
             }
-            if (t < t1) store_lanes<V>(y + t * C, o);
+            if (h + u < t1 - t0) store_lanes<V>(py + (long long)(h + u) * Ci, o);
             shift<V, W - 1>(win, cur);
         }
         if (h + U < kSeg)

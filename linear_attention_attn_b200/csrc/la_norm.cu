@@ -23,11 +23,16 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float act_f(float a, int silu) { return silu ? a * sigmoid_f(a) : a; }
-__device__ __forceinline__ float act_grad(float a, int silu) {
-    if (!silu) return 1.f;
-    const float s = sigmoid_f(a);
-    return s * fmaf(a, 1.f - s, 1.f);
+__device__ __forceinline__ float splat_like(float, float x) { return x; }
+__device__ __forceinline__ f2 splat_like(f2, float x) { return both(x); }
+// act(a), and g act'(a), of a float or a pair.
+template <typename E>
+__device__ __forceinline__ E act_of(E a, int silu) { return silu ? mul(a, sigmoid(a)) : a; }
+template <typename E>
+__device__ __forceinline__ E through_act(E g, E a, int silu) {
+    if (!silu) return g;
+    const E one = splat_like(a, 1.f), s = sigmoid(a), r = fma(s, splat_like(a, -1.f), one);
+    return mul(mul(g, s), fma(a, r, one));
 }
 
 // ------------------------------------------------------- groups in registers --
@@ -101,7 +106,7 @@ __global__ void __launch_bounds__(kSmallBlock) norm_small_fwd(NormArgs a, int L,
             for (int i = 0; i < V; ++i) {
                 const int ch = g * cg + c + i;
                 const float ga = a.gamma ? a.gamma[ch] : 1.f, be = a.beta ? a.beta[ch] : 0.f;
-                o[i] = act_f(fmaf((v[k][i] - mean) * rstd, ga, be), a.silu);
+                o[i] = act_of(fmaf((v[k][i] - mean) * rstd, ga, be), a.silu);
             }
             stv<V>(y + (long long)t * a.C + c, o);
         }
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kSmallBlock) norm_small_bwd(NormArgs a, int L,
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     xh[k][i] = (xh[k][i] - mean) * rstd;
-                    gr[k][i] *= act_grad(fmaf(xh[k][i], ga[k][i], be[k][i]), a.silu);
+                    gr[k][i] = through_act(gr[k][i], fmaf(xh[k][i], ga[k][i], be[k][i]), a.silu);
                     dbe[k][i] += gr[k][i];
                     dga[k][i] = fmaf(gr[k][i], xh[k][i], dga[k][i]);
                     gr[k][i] *= ga[k][i];
@@ -223,6 +228,8 @@ __device__ __forceinline__ void whereabouts(const Tiling &q, long long block, in
     b = (int)(block / q.tiles);
 }
 
+constexpr int kRows = 8;                   // rows that a thread has on their way at a time
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kTiledBlock) norm_stats(NormArgs a, Tiling q, float2 *part) {
     __shared__ float s_n[kTiledBlock], s_mean[kTiledBlock], s_m2[kTiledBlock];
@@ -232,23 +239,46 @@ __global__ void __launch_bounds__(kTiledBlock) norm_stats(NormArgs a, Tiling q, 
     const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
     const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
     const T *x = (const T *)a.x + (long long)b * a.T * a.C + (long long)g0 * cg;
+    typedef Lanes<V> L;
     float n = 0.f, s = 0.f, m2 = 0.f, pivot = 0.f;
-    if (r < q.rows && t0 + r < t1)
-        for (int v = v0; v < w; v += q.threads) {
-            if (n == 0.f) pivot = to_f(x[(long long)(t0 + r) * a.C + v * V]);
-#pragma unroll 8
-            for (int t = t0 + r; t < t1; t += q.rows) {
-                float e[V];
-                ldv<V>(x + (long long)t * a.C + v * V, e);
+    if (r < q.rows && t0 + r < t1) {
+        L ls, lq;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float d = e[i] - pivot;
-                    s += d;
-                    m2 = fmaf(d, d, m2);
-                }
-                n += V;
+        for (int i = 0; i < L::n; ++i) ls.e[i] = lq.e[i] = L::splat(0.f);
+        const long long step = (long long)q.rows * a.C;
+        for (int v = v0; v < w; v += q.threads) {
+            const T *p = x + (long long)(t0 + r) * a.C + v * V;
+            if (n == 0.f) pivot = to_f(*p);
+            const typename L::E minus = L::splat(-pivot);
+            const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
+            n += (float)rows * V;
+            for (int k = 0; k < rows; k += kRows) {
+                Raw<T, V> row[kRows];
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) row[u].load(p + u * step, k + u < rows);
+#pragma unroll
+                for (int u = 0; u < kRows; ++u)
+                    if (k + u < rows) {
+                        const L e = row[u].lanes();
+#pragma unroll
+                        for (int i = 0; i < L::n; ++i) {
+                            const auto d = add(e.e[i], minus);
+                            ls.e[i] = add(ls.e[i], d);
+                            lq.e[i] = fma(d, d, lq.e[i]);
+                        }
+                    }
+                p += kRows * step;
             }
         }
+        float vs[V], vq[V];
+        ls.get(vs);
+        lq.get(vq);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s += vs[i];
+            m2 += vq[i];
+        }
+    }
     s_n[threadIdx.x] = n;
     s_mean[threadIdx.x] = n > 0.f ? pivot + s / n : 0.f;
     s_m2[threadIdx.x] = n > 0.f ? m2 - s * (s / n) : 0.f;
@@ -271,6 +301,19 @@ __global__ void __launch_bounds__(kTiledBlock) norm_stats(NormArgs a, Tiling q, 
         sq = warp_sum(sq);
         if (lane == 0) part[((long long)b * q.tiles + tile) * a.G + g0 + j] = make_float2(mean, sq);
     }
+}
+
+// gamma (times a factor) and beta of V channels.
+template <int V>
+__device__ __forceinline__ void load_affine(const NormArgs &a, int c, float factor, Lanes<V> &ga, Lanes<V> &be) {
+    float g[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        g[i] = (a.gamma ? a.gamma[c + i] : 1.f) * factor;
+        b[i] = a.beta ? a.beta[c + i] : 0.f;
+    }
+    ga.set(g);
+    be.set(b);
 }
 
 template <typename T, int V>
@@ -307,26 +350,29 @@ __global__ void __launch_bounds__(kTiledBlock) norm_apply(NormArgs a, Tiling q, 
     const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
     if (r >= q.rows || t0 + r >= t1) return;
     const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
-    const int last = t0 + r + (t1 - 1 - t0 - r) / q.rows * q.rows;
+    typedef Lanes<V> L;
+    const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
+    const long long step = -(long long)q.rows * a.C;
     for (int v = v0; v < w; v += q.threads) {
         const int j = v / q.gl;
-        const float mean = s_mean[j], rstd = s_rstd[j];
-        float ga[V], be[V];
+        const float rstd = s_rstd[j];
+        const typename L::E minus = L::splat(-s_mean[j]);
+        L ga, be;
+        load_affine<V>(a, g0 * cg + v * V, rstd, ga, be);
+        long long o = base + v * V + (long long)(t0 + r) * a.C - (rows - 1) * step;      // the last row
+        for (int k = 0; k < rows; k += kRows) {
+            // all loads before the first store, which the compiler may not pass (y may be x)
+            Raw<T, V> row[kRows];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = g0 * cg + v * V + i;
-            ga[i] = (a.gamma ? a.gamma[c] : 1.f) * rstd;
-            be[i] = a.beta ? a.beta[c] : 0.f;
-        }
-        const T *x = (const T *)a.x + base + v * V;
-        T *y = (T *)a.y + base + v * V;
-#pragma unroll 4
-        for (int t = last; t >= t0; t -= q.rows) {
-            float e[V];
-            ldv<V>(x + (long long)t * a.C, e);
+            for (int u = 0; u < kRows; ++u) row[u].load((const T *)a.x + o + u * step, k + u < rows);
 #pragma unroll
-            for (int i = 0; i < V; ++i) e[i] = act_f(fmaf(e[i] - mean, ga[i], be[i]), a.silu);
-            stv<V>(y + (long long)t * a.C, e);
+            for (int u = 0; u < kRows; ++u) {
+                L e = row[u].lanes();
+#pragma unroll
+                for (int i = 0; i < L::n; ++i) e.e[i] = act_of(fma(add(e.e[i], minus), ga.e[i], be.e[i]), a.silu);
+                if (k + u < rows) store_lanes<V>((T *)a.y + o + u * step, e);
+            }
+            o += kRows * step;
         }
     }
 }
@@ -344,38 +390,53 @@ __global__ void __launch_bounds__(kTiledBlock) norm_bwd_sums(NormArgs a, Tiling 
     const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
     float2 *out = chan + ((long long)b * q.tiles + tile) * a.C + (long long)g0 * cg;
     float2 grp = make_float2(0.f, 0.f);
+    typedef Lanes<V> L;
     if (r < q.rows)
         for (int v = v0; v < w; v += q.threads) {
             const int j = v / q.gl;
             const float mean = a.mean_in[(long long)b * a.G + g0 + j], rstd = a.rstd_in[(long long)b * a.G + g0 + j];
-            float ga[V], be[V], dg[V], db[V];
+            const typename L::E minus = L::splat(-mean), scale = L::splat(rstd);
+            L ga, be, dg, db;
+            load_affine<V>(a, g0 * cg + v * V, 1.f, ga, be);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = g0 * cg + v * V + i;
-                ga[i] = a.gamma ? a.gamma[c] : 1.f;
-                be[i] = a.beta ? a.beta[c] : 0.f;
-                dg[i] = db[i] = 0.f;
-            }
-            const T *x = (const T *)a.x + base + v * V, *dy = (const T *)a.dy + base + v * V;
-#pragma unroll 4
-            for (int t = t0 + r; t < t1; t += q.rows) {
-                float e[V], d[V];
-                ldv<V>(x + (long long)t * a.C, e);
-                ldv<V>(dy + (long long)t * a.C, d);
+            for (int i = 0; i < L::n; ++i) dg.e[i] = db.e[i] = L::splat(0.f);
+            const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
+            const long long step = (long long)q.rows * a.C;
+            const T *x = (const T *)a.x + base + (long long)(t0 + r) * a.C + v * V;
+            const T *dy = (const T *)a.dy + base + (long long)(t0 + r) * a.C + v * V;
+            constexpr int U = kRows / 2;
+            for (int k = 0; k < rows; k += U) {
+                Raw<T, V> rx[U], rg[U];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = (e[i] - mean) * rstd;
-                    const float g = d[i] * act_grad(fmaf(xh, ga[i], be[i]), a.silu);
-                    db[i] += g;
-                    dg[i] = fmaf(g, xh, dg[i]);
+                for (int u = 0; u < U; ++u) {
+                    rx[u].load(x + u * step, k + u < rows);
+                    rg[u].load(dy + u * step, k + u < rows);           // 0 behind the tile: adds nothing
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const L e = rx[u].lanes(), d = rg[u].lanes();
+#pragma unroll
+                    for (int i = 0; i < L::n; ++i) {
+                        const auto xh = mul(add(e.e[i], minus), scale);
+                        auto g = through_act(d.e[i], fma(xh, ga.e[i], be.e[i]), a.silu);
+                        if (k + u >= rows) g = L::splat(0.f);
+                        db.e[i] = add(db.e[i], g);
+                        dg.e[i] = fma(g, xh, dg.e[i]);
+                    }
+                }
+                x += U * step;
+                dy += U * step;
             }
+            float vga[V], vdg[V], vdb[V];
+            ga.get(vga);
+            dg.get(vdg);
+            db.get(vdb);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                grp.x = fmaf(ga[i], db[i], grp.x);
-                grp.y = fmaf(ga[i], dg[i], grp.y);
-                if (q.rows == 1) out[v * V + i] = make_float2(dg[i], db[i]);
-                else s_c[(r * q.w + v) * V + i] = make_float2(dg[i], db[i]);
+                grp.x = fmaf(vga[i], vdb[i], grp.x);
+                grp.y = fmaf(vga[i], vdg[i], grp.y);
+                if (q.rows == 1) out[v * V + i] = make_float2(vdg[i], vdb[i]);
+                else s_c[(r * q.w + v) * V + i] = make_float2(vdg[i], vdb[i]);
             }
         }
     s_g[threadIdx.x] = grp;
@@ -439,32 +500,39 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
     const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
     if (r >= q.rows || t0 + r >= t1) return;
     const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
-    const int last = t0 + r + (t1 - 1 - t0 - r) / q.rows * q.rows;
+    typedef Lanes<V> L;
+    const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
+    const long long step = -(long long)q.rows * a.C;
     for (int v = v0; v < w; v += q.threads) {
         const int j = v / q.gl;
         const float mean = a.mean_in[(long long)b * a.G + g0 + j], rstd = a.rstd_in[(long long)b * a.G + g0 + j];
-        const float m0 = s_m0[j], m1 = s_m1[j];
-        float ga[V], be[V];
+        const typename L::E minus = L::splat(-mean), scale = L::splat(rstd), m0 = L::splat(-s_m0[j]),
+                            m1 = L::splat(-s_m1[j]);
+        L ga, be;
+        load_affine<V>(a, g0 * cg + v * V, 1.f, ga, be);
+        long long o = base + v * V + (long long)(t0 + r) * a.C - (rows - 1) * step;      // the last row
+        constexpr int U = kRows / 2;
+        for (int k = 0; k < rows; k += U) {
+            // all loads before the first store, which the compiler may not pass (dx may be dy)
+            Raw<T, V> rx[U], rg[U];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = g0 * cg + v * V + i;
-            ga[i] = a.gamma ? a.gamma[c] : 1.f;
-            be[i] = a.beta ? a.beta[c] : 0.f;
-        }
-        const T *x = (const T *)a.x + base + v * V, *dy = (const T *)a.dy + base + v * V;
-        T *dx = (T *)a.dx + base + v * V;
-#pragma unroll 4
-        for (int t = last; t >= t0; t -= q.rows) {
-            float e[V], d[V];
-            ldv<V>(x + (long long)t * a.C, e);
-            ldv<V>(dy + (long long)t * a.C, d);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float xh = (e[i] - mean) * rstd;
-                const float g = d[i] * act_grad(fmaf(xh, ga[i], be[i]), a.silu) * ga[i];
-                d[i] = rstd * (g - m0 - xh * m1);
+            for (int u = 0; u < U; ++u) {
+                rx[u].load((const T *)a.x + o + u * step, k + u < rows);
+                rg[u].load((const T *)a.dy + o + u * step, k + u < rows);
             }
-            stv<V>(dx + (long long)t * a.C, d);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const L e = rx[u].lanes();
+                L d = rg[u].lanes();
+#pragma unroll
+                for (int i = 0; i < L::n; ++i) {
+                    const auto xh = mul(add(e.e[i], minus), scale);
+                    const auto g = through_act(d.e[i], fma(xh, ga.e[i], be.e[i]), a.silu);
+                    d.e[i] = mul(scale, fma(xh, m1, fma(g, ga.e[i], m0)));
+                }
+                if (k + u < rows) store_lanes<V>((T *)a.dx + o + u * step, d);
+            }
+            o += U * step;
         }
     }
 }
