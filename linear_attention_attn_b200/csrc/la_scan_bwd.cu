@@ -11,10 +11,10 @@
 //
 // Nothing is kept from the forward.  A block owns a tile of channels (as in the forward, LN lanes a
 // channel) and a segment of the sequence; it walks forwards once, leaving the state before every
-// tile of kTile tokens in the workspace, then backwards tile by tile: the tile's states and decays
-// are formed again in registers (one exponential each) and used in reverse order.  So a state costs
-// two exponentials and about 12 multiply-adds, and 8 / kTile bytes of workspace traffic each way:
-// the kernel is bound by instruction issue, not by HBM.  The sums over channels of dB and dC are
+// kSub tokens in the workspace, then backwards, kSub tokens at a time: their states and decays are
+// formed again in registers (one exponential each) and used in reverse order.  So a state costs two
+// exponentials and about 12 multiply-adds, and 4 / kSub bytes of workspace traffic each way: the
+// kernel is bound by instruction issue, not by HBM.  The sums over channels of dB and dC are
 // butterflies over the lanes of a warp (each step hands half of the values to the partner), then
 // over the block's warps in shared memory, then over the channel tiles in a last launch, always in
 // the same order; that launch also joins the batch entries' parts of dA, dD and dbias.
@@ -29,124 +29,188 @@ namespace {
 
 using namespace scan;
 
+constexpr int kSub = 8;            // tokens whose states and decays are in registers at a time
+
 template <int LN> struct Cfg {
     static constexpr int threads = LN == 1 ? 128 : 256;
     static constexpr int warps = threads / 32;
     static constexpr int width = threads / LN;
     static constexpr int NP = kNS * LN;
-    static constexpr int per = kTile * width / threads;
-    static constexpr int bc_per = (kTile * NP + threads - 1) / threads;
-    // floats of shared memory: per pair (d, u, e, x) and (sigma', dy silu') twice, B and C twice,
-    // three sums per pair, the warps' sums of dC and dB
-    static constexpr int pairs = kTile * width;
-    static constexpr size_t smem =
-        sizeof(float) * (2 * pairs * 6 + 2 * 2 * kTile * NP + 3 * pairs + warps * kTile * 2 * NP);
+    static constexpr int pairs = kTile * width;             // (token, channel)
+    static constexpr int quads = pairs / 4;
+    static constexpr int per = (quads + threads - 1) / threads;
+    static constexpr int bquads = kTile * LN;
+    static constexpr int bper = (bquads + threads - 1) / threads;
+    static constexpr int kept = LN >= 16 ? 4 : LN == 8 ? 2 : 1;   // sums over channels that a lane ends up with
+    // planes d, u, e (pairs, twice), B and C (pairs, twice), the quads' own (four floats, twice), the
+    // three sums over states, the warps' sums of dC and dB
+    static constexpr size_t smem = sizeof(f2) * (6 * pairs + 8 * kTile * LN) +
+                                   sizeof(float) * (8 * pairs + 3 * pairs + warps * kTile * 2 * NP);
 };
 
 struct Seg {
     int segs, len;
     float *S, *R, *sum;            // [B, segs, C, N] twice, [B, segs, C]
-    float *ckpt;                   // [B, ceil(T / kTile), C, N]
+    float *ckpt;                   // [B, ceil(T / kSub), C, N]
     float *bc;                     // [tiles][2][B T G N]: the channel tiles' parts of dC and dB
     float *pA, *pD, *pbias;        // [B segs][C N], [B segs][C] twice
+    int vec, bvec;                 // rows of the [B,T,C] tensors (of Bm, Cm) allow accesses of 4 elements
 };
 
 template <int LN>
 struct Smem {
     using K = Cfg<LN>;
-    float4 *in;                    // [2][kTile][width]: d, u, e, x
-    float2 *ex;                    // [2][kTile][width]: sigma(dt + bias) (1 without softplus), dy silu'(z)
-    float *B, *C;                  // [2][kTile][NP]
+    // As in the forward, what a pair of states shares lies twice side by side, B and C in two planes.
+    f2 *d, *u, *e;                 // [2][kTile][width]
+    f2 *B, *C;                     // [2][kTile][2][LN]
+    float4 *own;                   // [2][4][quads]: sigma(dt + bias) (1 without softplus), dy silu'(z), d, e
     float *o;                      // [3][kTile][width]: sum_n C h, q, sum_n A p (in units of 1 / log2 e)
     float *red;                    // [warps][kTile][2][NP]
     __device__ explicit Smem(float *p) {
-        in = reinterpret_cast<float4 *>(p);
-        ex = reinterpret_cast<float2 *>(p + 2 * K::pairs * 4);
-        B = p + 2 * K::pairs * 6;
-        C = B + 2 * kTile * K::NP;
-        o = C + 2 * kTile * K::NP;
+        own = reinterpret_cast<float4 *>(p);
+        d = reinterpret_cast<f2 *>(p + 8 * K::pairs);
+        u = d + 2 * K::pairs;
+        e = u + 2 * K::pairs;
+        B = e + 2 * K::pairs;
+        C = B + 4 * kTile * LN;
+        o = reinterpret_cast<float *>(C + 4 * kTile * LN);
         red = o + 3 * K::pairs;
     }
 };
 
 // Stages tiles of kTile tokens: load() fetches one into registers, store() converts it into shared
-// memory.  BACK: with dy, z and C; else x, dt and B only.
+// memory.  BACK: with dy, z and C; else x, dt and B only.  A thread's quads are all of the same four
+// channels.
 template <typename T, int LN, bool BACK>
 struct Stager {
     using K = Cfg<LN>;
-    T rx[K::per], rd[K::per], rz[K::per], rg[K::per], rB[K::bc_per], rC[K::bc_per];
-    __device__ __forceinline__ void load(const ScanArgs &a, const Place &p, int tb, int n) {
-        const int tid = threadIdx.x;
+    static constexpr int row = K::width / 4, t_step = K::threads / row, b_step = K::threads / LN;
+    Quad<T> rx[K::per], rd[K::per], rz[K::per], rg[K::per], rB[K::bper], rC[K::bper];
+    const ScanArgs &a;
+    const Seg &sg;
+    int c, have, t_first, b_first, b_have, n;
+    long long x0, xs, b0, bs;      // element offsets of the thread's first quad at token 0, steps between quads
+    f2 bias[2];
+
+    __device__ __forceinline__ Stager(const ScanArgs &a_, const Seg &sg_, const Place &p, int n_) : a(a_), sg(sg_), n(n_) {
+        const int tid = threadIdx.x, m = tid % LN * 4;
         const long long row0 = (long long)p.b * a.T;
+        c = tid % row * 4;
+        have = p.nc - c;
+        t_first = tid / row;
+        b_first = tid / LN;
+        b_have = a.N - m;
+        x0 = (row0 + t_first) * a.C + p.c0 + c;
+        xs = (long long)t_step * a.C;
+        b0 = ((row0 + b_first) * a.G + p.g) * a.N + m;
+        bs = (long long)b_step * a.G * a.N;
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < K::per; ++i) {
-            const int e = tid + i * K::threads, t = tb + e / K::width, c = e % K::width;
-            rx[i] = rd[i] = rz[i] = rg[i] = from_f<T>(0.f);
-            if (t < n && c < p.nc) {
-                const long long o = (row0 + t) * a.C + p.c0 + c;
-                rx[i] = ((const T *)a.x)[o];
-                rd[i] = ((const T *)a.dt_in)[o];
-                if (BACK) {
-                    rg[i] = ((const T *)a.dy)[o];
-                    if (a.z) rz[i] = ((const T *)a.z)[o];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < K::bc_per; ++i) {
-            const int e = tid + i * K::threads, t = tb + e / K::NP, m = e % K::NP;
-            rB[i] = rC[i] = from_f<T>(0.f);
-            if (e < kTile * K::NP && t < n && m < a.N) {
-                const long long o = ((row0 + t) * a.G + p.g) * a.N + m;
-                rB[i] = ((const T *)a.Bm)[o];
-                if (BACK) rC[i] = ((const T *)a.Cm)[o];
-            }
-        }
+        for (int j = 0; j < 4; ++j) v[j] = a.dt_bias && j < have ? a.dt_bias[p.c0 + c + j] : 0.f;
+        bias[0] = pack2(v[0], v[1]);
+        bias[1] = pack2(v[2], v[3]);
     }
-    __device__ __forceinline__ void store(const ScanArgs &a, const Place &p, int tb, int n, Smem<LN> &s, int buf) {
-        const int tid = threadIdx.x;
+    static __device__ __forceinline__ bool mine(int i) { return K::quads % K::threads == 0 || (int)threadIdx.x + i * K::threads < K::quads; }
+    static __device__ __forceinline__ bool mine_b(int i) { return K::bquads % K::threads == 0 || (int)threadIdx.x + i * K::threads < K::bquads; }
+
+    __device__ __forceinline__ void load(int tb) {
+        const long long xo = x0 + (long long)tb * a.C, bo = b0 + (long long)tb * a.G * a.N;
 #pragma unroll
-        for (int i = 0; i < K::per; ++i) {
-            const int e = tid + i * K::threads, t = tb + e / K::width, c = e % K::width;
-            float4 in = make_float4(0.f, 0.f, 0.f, 0.f);
-            float2 ex = make_float2(1.f, 0.f);
-            if (t < n && c < p.nc) {
-                const float x = to_f(rx[i]);
-                float d = to_f(rd[i]) + (a.dt_bias ? a.dt_bias[p.c0 + c] : 0.f);
-                if (a.softplus) {
-                    if (BACK) ex.x = sigmoid_f(d);
-                    d = softplus_f(d);
-                }
-                in = make_float4(d, d * x, 0.f, x);
+        for (int i = 0; i < K::per; ++i)
+            if (mine(i)) {
+                const int live = tb + t_first + i * t_step < n ? have : 0;
+                rx[i].load((const T *)a.x + xo + i * xs, live, sg.vec);
+                rd[i].load((const T *)a.dt_in + xo + i * xs, live, sg.vec);
                 if (BACK) {
-                    in.z = to_f(rg[i]);
-                    if (a.z) {
-                        const float z = to_f(rz[i]), sg = sigmoid_f(z);
-                        ex.y = in.z * sg * fmaf(z, 1.f - sg, 1.f);
-                        in.z *= z * sg;
-                    }
+                    rg[i].load((const T *)a.dy + xo + i * xs, live, sg.vec);
+                    if (a.z) rz[i].load((const T *)a.z + xo + i * xs, live, sg.vec);
                 }
             }
-            s.in[buf * K::pairs + e] = in;
-            if (BACK) s.ex[buf * K::pairs + e] = ex;
-        }
 #pragma unroll
-        for (int i = 0; i < K::bc_per; ++i) {
-            const int e = tid + i * K::threads;
-            if (e < kTile * K::NP) {
-                s.B[buf * kTile * K::NP + e] = to_f(rB[i]);
-                if (BACK) s.C[buf * kTile * K::NP + e] = to_f(rC[i]);
+        for (int i = 0; i < K::bper; ++i)
+            if (mine_b(i)) {
+                const int live = tb + b_first + i * b_step < n ? b_have : 0;
+                rB[i].load((const T *)a.Bm + bo + i * bs, live, sg.bvec);
+                if (BACK) rC[i].load((const T *)a.Cm + bo + i * bs, live, sg.bvec);
             }
-        }
+    }
+    static __device__ __forceinline__ void twice(f2 *plane, int at, f2 v) {
+        float x, y;
+        unpack2(v, x, y);
+        *reinterpret_cast<ulonglong2 *>(plane + at) = make_ulonglong2(both(x), both(y));
+    }
+    __device__ __forceinline__ void store(int tb, Smem<LN> &s, int buf) {
+#pragma unroll
+        for (int i = 0; i < K::per; ++i)
+            if (mine(i)) {
+                const int at = threadIdx.x + i * K::threads;
+                const bool gone = tb + t_first + i * t_step >= n;         // behind the end: the state stays
+                f2 d[2], x[2], sig[2] = {both(1.f), both(1.f)};
+                rd[i].values(d);
+                rx[i].values(x);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    d[j] = add2(d[j], bias[j]);
+                    if (a.softplus) {
+                        const f2 e = exp_neg_abs(d[j]);
+                        if (BACK) {
+                            // sigma(r): 1 / (1 + e) for r >= 0, e / (1 + e) below
+                            float r0, r1, e0, e1, q0, q1;
+                            unpack2(d[j], r0, r1);
+                            unpack2(e, e0, e1);
+                            unpack2(add2(e, both(1.f)), q0, q1);
+                            sig[j] = pack2((r0 < 0.f ? e0 : 1.f) * rcp(q0), (r1 < 0.f ? e1 : 1.f) * rcp(q1));
+                        }
+                        d[j] = softplus_from(d[j], e);
+                    }
+                    if (gone) d[j] = 0;
+                    twice(s.d, buf * K::pairs + 4 * at + 2 * j, d[j]);
+                    twice(s.u, buf * K::pairs + 4 * at + 2 * j, mul2(d[j], x[j]));
+                }
+                if (BACK) {
+                    f2 g[2], z[2], dz[2] = {0, 0};
+                    rg[i].values(g);
+                    if (a.z) {
+                        rz[i].values(z);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            // silu'(z) = sg (1 + z (1 - sg))
+                            const f2 sg_ = sigmoid2(z[j]), gs = mul2(g[j], sg_);
+                            dz[j] = mul2(gs, fma2(z[j], fma2(sg_, both(-1.f), both(1.f)), both(1.f)));
+                            g[j] = mul2(gs, z[j]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) twice(s.e, buf * K::pairs + 4 * at + 2 * j, g[j]);
+                    ulonglong2 *own = reinterpret_cast<ulonglong2 *>(s.own) + buf * 4 * K::quads + at;
+                    own[0] = make_ulonglong2(sig[0], sig[1]);
+                    own[K::quads] = make_ulonglong2(dz[0], dz[1]);
+                    own[2 * K::quads] = make_ulonglong2(d[0], d[1]);
+                    own[3 * K::quads] = make_ulonglong2(g[0], g[1]);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < K::bper; ++i)
+            if (mine_b(i)) {
+                f2 v[2];
+                const int at = (buf * kTile + b_first + i * b_step) * 2 * LN + threadIdx.x % LN;
+                rB[i].values(v);
+                s.B[at] = v[0];
+                s.B[at + LN] = v[1];
+                if (BACK) {
+                    rC[i].values(v);
+                    s.C[at] = v[0];
+                    s.C[at + LN] = v[1];
+                }
+            }
     }
 };
 
-// Sums v[0..7] over the 32 / LN channels of a warp (lanes of equal nl) and leaves each sum in `out`
-// at [quantity][state], quantity 0 from v[0..3] and 1 from v[4..7].
+// Sums v[0..7] over the 32 / LN channels of a warp (lanes of equal nl): each step hands half of the
+// values to the partner.  Afterwards a lane's first Cfg::kept values are sums of the quantities
+// from where_reduced() on, for the states of its nl.
 template <int LN>
-__device__ __forceinline__ void reduce_channels(float (&v)[8], int lane, int nl, float *out) {
-    constexpr int NP = kNS * LN;
-    int base = 0;
+__device__ __forceinline__ void reduce_channels(float (&v)[8], int lane) {
     {
         const bool hi = lane & LN;
 #pragma unroll
@@ -154,7 +218,6 @@ __device__ __forceinline__ void reduce_channels(float (&v)[8], int lane, int nl,
             const float s = hi ? v[i] : v[i + 4];
             v[i] = (hi ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, s, LN);
         }
-        base = hi ? NP : 0;
     }
     if (LN <= 8) {
         const bool hi = lane & (2 * LN);
@@ -163,20 +226,18 @@ __device__ __forceinline__ void reduce_channels(float (&v)[8], int lane, int nl,
             const float s = hi ? v[i] : v[i + 2];
             v[i] = (hi ? v[i + 2] : v[i]) + __shfl_xor_sync(0xffffffffu, s, 2 * LN);
         }
-        base += hi ? 2 : 0;
     }
     if (LN <= 4) {
         const bool hi = lane & (4 * LN);
         const float s = hi ? v[0] : v[1];
         v[0] = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, s, 4 * LN);
-        base += hi ? 1 : 0;
     }
     if (LN <= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8 * LN);
     if (LN <= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16 * LN);
-    constexpr int kept = LN >= 16 ? 4 : LN == 8 ? 2 : 1;
-    if (LN <= 2 && lane >= 8 * LN) return;
-#pragma unroll
-    for (int i = 0; i < kept; ++i) out[base + nl * kNS + i] = v[i];
+}
+template <int LN>
+__device__ __forceinline__ int where_reduced(int lane) {
+    return (lane & LN ? 4 : 0) + (LN <= 8 && lane & (2 * LN) ? 2 : 0) + (LN <= 4 && lane & (4 * LN) ? 1 : 0);
 }
 
 // First launch of the segmented form: (S, R, sum of d) of every segment.
@@ -190,44 +251,47 @@ scan_bwd_ends(ScanArgs a, Seg sg, int tiles) {
     const int nl = threadIdx.x % LN, ch = threadIdx.x / LN, n0 = nl * kNS;
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
-    float A2[kNS] = {}, h[kNS] = {}, P[kNS], R[kNS] = {}, sum = 0.f;
-    if (live) load_states(a.A + c * a.N, n0, a.N, A2);
-#pragma unroll
-    for (int k = 0; k < kNS; ++k) {
-        A2[k] *= kLog2e;
-        P[k] = 1.f;
-    }
+    float A4[kNS] = {}, sum = 0.f;
+    if (live) load_states(a.A + c * a.N, n0, a.N, A4);
+    const f2 A2[2] = {mul2(pack2(A4[0], A4[1]), both(kLog2e)), mul2(pack2(A4[2], A4[3]), both(kLog2e))};
+    f2 h[2] = {0, 0}, P[2] = {both(1.f), both(1.f)}, R[2] = {0, 0};
     const int t0 = p.seg * sg.len, n = min(seq_end(a.lengths, p.b, a.T), min(a.T, t0 + sg.len));
     const int count = n > t0 ? (n - t0 + kTile - 1) / kTile : 0;
-    Stager<T, LN, true> stg;
+    Stager<T, LN, true> stg(a, sg, p, n);
     if (count > 0) {
-        stg.load(a, p, t0, n);
-        stg.store(a, p, t0, n, s, 0);
+        stg.load(t0);
+        stg.store(t0, s, 0);
     }
     for (int tile = 0; tile < count; ++tile) {
         __syncthreads();
         const int buf = tile & 1;
-        if (tile + 1 < count) stg.load(a, p, t0 + (tile + 1) * kTile, n);
-        const float4 *in = s.in + buf * K::pairs + ch;
-        const float *sB = s.B + buf * kTile * K::NP + n0, *sC = s.C + buf * kTile * K::NP + n0;
-#pragma unroll 4
-        for (int j = 0; j < kTile; ++j) {
-            const float4 v = in[j * K::width];
-            sum += v.x;
+        if (tile + 1 < count) stg.load(t0 + (tile + 1) * kTile);
+        const int at = buf * K::pairs + ch, bt = buf * kTile * 2 * LN + nl;
 #pragma unroll
-            for (int k = 0; k < kNS; ++k) {
-                const float e = ex2(v.x * A2[k]);
-                h[k] = fmaf(e, h[k], v.y * sB[j * K::NP + k]);
-                P[k] *= e;
-                R[k] = fmaf(P[k], v.z * sC[j * K::NP + k], R[k]);
+        for (int j = 0; j < kTile; ++j) {
+            const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width], e = s.e[at + j * K::width];
+            float d0, d1;
+            unpack2(d, d0, d1);
+            sum += d0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f2 E = ex2_2(mul2(d, A2[k]));
+                h[k] = fma2(E, h[k], mul2(u, s.B[bt + (2 * j + k) * LN]));
+                P[k] = mul2(P[k], E);
+                R[k] = fma2(P[k], mul2(e, s.C[bt + (2 * j + k) * LN]), R[k]);
             }
         }
-        if (tile + 1 < count) stg.store(a, p, t0 + (tile + 1) * kTile, n, s, buf ^ 1);
+        if (tile + 1 < count) stg.store(t0 + (tile + 1) * kTile, s, buf ^ 1);
     }
     if (!live) return;
     const long long at = ((long long)p.b * sg.segs + p.seg) * a.C + c;
-    store_states(sg.S + at * a.N, n0, a.N, h);
-    store_states(sg.R + at * a.N, n0, a.N, R);
+    float v[4];
+    unpack2(h[0], v[0], v[1]);
+    unpack2(h[1], v[2], v[3]);
+    store_states(sg.S + at * a.N, n0, a.N, v);
+    unpack2(R[0], v[0], v[1]);
+    unpack2(R[1], v[2], v[3]);
+    store_states(sg.R + at * a.N, n0, a.N, v);
     if (nl == 0) sg.sum[at] = sum;
 }
 
@@ -242,164 +306,223 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
     const int nl = tid % LN, ch = tid / LN, n0 = nl * kNS;
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
-    float A2[kNS] = {}, h[kNS] = {}, w[kNS] = {};
-    if (live) {
-        load_states(a.A + c * a.N, n0, a.N, A2);
+    f2 A2[2], h[2], w[2];
+    {
+        float A4[kNS] = {}, h4[kNS] = {}, w4[kNS] = {};
+        if (live) {
+            load_states(a.A + c * a.N, n0, a.N, A4);
 #pragma unroll
-        for (int k = 0; k < kNS; ++k) A2[k] *= kLog2e;
-        // the state before this segment and the gradient of the state after it
-        const long long bc = ((long long)p.b * a.C + c) * a.N;
-        if (a.state_in) load_states(a.state_in + bc, n0, a.N, h);
-        if (a.dstate_in) load_states(a.dstate_in + bc, n0, a.N, w);
-        const long long at = (long long)p.b * sg.segs * a.C + c;
-        for (int i = 0; i < p.seg; ++i) {
-            const long long q = at + (long long)i * a.C;
-            const float d = sg.sum[q];
-            float S[kNS];
-            load_states(sg.S + q * a.N, n0, a.N, S);
+            for (int k = 0; k < kNS; ++k) A4[k] *= kLog2e;
+            // the state before this segment and the gradient of the state after it
+            const long long bc = ((long long)p.b * a.C + c) * a.N;
+            if (a.state_in) load_states(a.state_in + bc, n0, a.N, h4);
+            if (a.dstate_in) load_states(a.dstate_in + bc, n0, a.N, w4);
+            const long long at = (long long)p.b * sg.segs * a.C + c;
+            for (int i = 0; i < p.seg; ++i) {
+                const long long q = at + (long long)i * a.C;
+                const float d = sg.sum[q];
+                float S[kNS];
+                load_states(sg.S + q * a.N, n0, a.N, S);
 #pragma unroll
-            for (int k = 0; k < kNS; ++k) h[k] = fmaf(ex2(d * A2[k]), h[k], S[k]);
+                for (int k = 0; k < kNS; ++k) h4[k] = fmaf(ex2(d * A4[k]), h4[k], S[k]);
+            }
+            for (int i = sg.segs - 1; i > p.seg; --i) {
+                const long long q = at + (long long)i * a.C;
+                const float d = sg.sum[q];
+                float R[kNS];
+                load_states(sg.R + q * a.N, n0, a.N, R);
+#pragma unroll
+                for (int k = 0; k < kNS; ++k) w4[k] = fmaf(ex2(d * A4[k]), w4[k], R[k]);
+            }
         }
-        for (int i = sg.segs - 1; i > p.seg; --i) {
-            const long long q = at + (long long)i * a.C;
-            const float d = sg.sum[q];
-            float R[kNS];
-            load_states(sg.R + q * a.N, n0, a.N, R);
 #pragma unroll
-            for (int k = 0; k < kNS; ++k) w[k] = fmaf(ex2(d * A2[k]), w[k], R[k]);
+        for (int k = 0; k < 2; ++k) {
+            A2[k] = pack2(A4[2 * k], A4[2 * k + 1]);
+            h[k] = pack2(h4[2 * k], h4[2 * k + 1]);
+            w[k] = pack2(w4[2 * k], w4[2 * k + 1]);
         }
     }
     const int t0 = p.seg * sg.len, t1 = min(a.T, t0 + sg.len), n = min(seq_end(a.lengths, p.b, a.T), t1);
     const int count = n > t0 ? (n - t0 + kTile - 1) / kTile : 0;
-    const long long tiles_t = (a.T + kTile - 1) / kTile;
-    // this lane's states before tile i of the segment
-    float *ck = sg.ckpt + (((long long)p.b * tiles_t + t0 / kTile) * a.C + c) * a.N;
+    const long long subs_t = (a.T + kSub - 1) / kSub;
+    // this lane's states before sub-tile i of the segment
+    float *ck = sg.ckpt + (((long long)p.b * subs_t + t0 / kSub) * a.C + c) * a.N;
     const long long ck_step = (long long)a.C * a.N;
+    const int subs = count > 0 ? (n - t0 + kSub - 1) / kSub : 0;
 
-    // ---- forwards: the state before every tile
+    // ---- forwards: the state before every sub-tile
     {
-        Stager<T, LN, false> stg;
-        if (count > 1) {
-            stg.load(a, p, t0, n);
-            stg.store(a, p, t0, n, s, 0);
+        Stager<T, LN, false> stg(a, sg, p, n);
+        if (count > 0) {
+            stg.load(t0);
+            stg.store(t0, s, 0);
         }
         for (int tile = 0; tile < count; ++tile) {
-            if (live) store_states(ck + tile * ck_step, n0, a.N, h);
-            if (tile + 1 == count) break;
             __syncthreads();
             const int buf = tile & 1;
-            if (tile + 2 < count) stg.load(a, p, t0 + (tile + 1) * kTile, n);
-            const float4 *in = s.in + buf * K::pairs + ch;
-            const float *sB = s.B + buf * kTile * K::NP + n0;
+            if (tile + 1 < count) stg.load(t0 + (tile + 1) * kTile);
+            const int at = buf * K::pairs + ch, bt = buf * kTile * 2 * LN + nl;
+            f2 mid[kTile / kSub][2];
 #pragma unroll
             for (int j = 0; j < kTile; ++j) {
-                const float2 v = *reinterpret_cast<const float2 *>(in + j * K::width);
-                const float4 B4 = *reinterpret_cast<const float4 *>(sB + j * K::NP);
-                const float Bk[4] = {B4.x, B4.y, B4.z, B4.w};
+                const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width];
 #pragma unroll
-                for (int k = 0; k < kNS; ++k) h[k] = fmaf(ex2(v.x * A2[k]), h[k], v.y * Bk[k]);
+                for (int k = 0; k < 2; ++k) {
+                    if (j % kSub == 0) mid[j / kSub][k] = h[k];
+                    h[k] = fma2(ex2_2(mul2(d, A2[k])), h[k], mul2(u, s.B[bt + (2 * j + k) * LN]));
+                }
             }
-            if (tile + 2 < count) stg.store(a, p, t0 + (tile + 1) * kTile, n, s, buf ^ 1);
+#pragma unroll
+            for (int i = 0; i < kTile / kSub; ++i)
+                if (live && tile * (kTile / kSub) + i < subs) {
+                    float v[4];
+                    unpack2(mid[i][0], v[0], v[1]);
+                    unpack2(mid[i][1], v[2], v[3]);
+                    store_states(ck + (tile * (kTile / kSub) + i) * ck_step, n0, a.N, v);
+                }
+            if (tile + 1 < count) stg.store(t0 + (tile + 1) * kTile, s, buf ^ 1);
         }
         __syncthreads();
     }
 
     // ---- backwards
-    float dA[kNS] = {}, dD = 0.f, dbias = 0.f;
-    const long long row0 = (long long)p.b * a.T;
-    Stager<T, LN, true> stg;
+    const bool gated = a.z != nullptr;
+    f2 dA[2] = {0, 0}, dD[2] = {0, 0}, dbias[2] = {0, 0}, Dc[2];
+    Stager<T, LN, true> stg(a, sg, p, n);
+    {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = a.D && j < stg.have ? a.D[p.c0 + stg.c + j] : 0.f;
+        Dc[0] = pack2(v[0], v[1]);
+        Dc[1] = pack2(v[2], v[3]);
+    }
     if (count > 0) {
-        stg.load(a, p, t0 + (count - 1) * kTile, n);
-        stg.store(a, p, t0 + (count - 1) * kTile, n, s, (count - 1) & 1);
+        stg.load(t0 + (count - 1) * kTile);
+        stg.store(t0 + (count - 1) * kTile, s, (count - 1) & 1);
     }
     __syncthreads();
     for (int tile = count - 1; tile >= 0; --tile) {
         const int buf = tile & 1, tb = t0 + tile * kTile;
-        if (tile > 0) stg.load(a, p, tb - kTile, n);
-        const float4 *in = s.in + buf * K::pairs + ch;
-        const float *sB = s.B + buf * kTile * K::NP + n0, *sC = s.C + buf * kTile * K::NP + n0;
-        float hs[kNS] = {};
-        if (live) load_states(ck + tile * ck_step, n0, a.N, hs);
-        float H[kTile][kNS], E[kTile][kNS];
+        float hs4[kTile / kSub][kNS] = {};
 #pragma unroll
-        for (int q = 0; q < kTile; q += 4) {
-            float ys[4];
+        for (int i = 0; i < kTile / kSub; ++i)
+            if (live && tile * (kTile / kSub) + i < subs)
+                load_states(ck + (tile * (kTile / kSub) + i) * ck_step, n0, a.N, hs4[i]);
+        Quad<T> kx[K::per];                                   // this tile's x, for its outputs
 #pragma unroll
-            for (int j = q; j < q + 4; ++j) {
-                const float2 v = *reinterpret_cast<const float2 *>(in + j * K::width);
-                const float4 B4 = *reinterpret_cast<const float4 *>(sB + j * K::NP);
-                const float4 C4 = *reinterpret_cast<const float4 *>(sC + j * K::NP);
-                const float Bk[4] = {B4.x, B4.y, B4.z, B4.w};
+        for (int i = 0; i < K::per; ++i) kx[i] = stg.rx[i];
+        if (tile > 0) stg.load(tb - kTile);
 #pragma unroll
-                for (int k = 0; k < kNS; ++k) {
-                    E[j][k] = ex2(v.x * A2[k]);
-                    H[j][k] = fmaf(E[j][k], j ? H[j - 1][k] : hs[k], v.y * Bk[k]);
+        for (int sub = kTile / kSub - 1; sub >= 0; --sub) {
+            const int at = buf * K::pairs + sub * kSub * K::width + ch, bt = (buf * kTile + sub * kSub) * 2 * LN + nl;
+            const f2 hs[2] = {pack2(hs4[sub][0], hs4[sub][1]), pack2(hs4[sub][2], hs4[sub][3])};
+            f2 H[kSub][2], E[kSub][2];
+            float ys[kSub / 4][4], lb[kSub / 4][4], dd[kSub / 4][4], sums[kSub][K::kept];
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+                const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    E[j][k] = ex2_2(mul2(d, A2[k]));
+                    H[j][k] = fma2(E[j][k], j ? H[j - 1][k] : hs[k], mul2(u, s.B[bt + (2 * j + k) * LN]));
                 }
-                ys[j - q] = fmaf(C4.x, H[j][0], fmaf(C4.y, H[j][1], fmaf(C4.z, H[j][2], C4.w * H[j][3])));
-            }
-            if (a.z) {
-                reduce4<LN>(ys, nl);
-                if (LN <= 4 || nl < 4) {
-#pragma unroll
-                    for (int j = 0; j < Kept<LN>::value; ++j)
-                        s.o[(q + first_token<LN>(nl) + j) * K::width + ch] = ys[j];
+                if (gated) {
+                    float y0, y1;
+                    unpack2(fma2(s.C[bt + 2 * j * LN], H[j][0], mul2(s.C[bt + (2 * j + 1) * LN], H[j][1])), y0, y1);
+                    ys[j / 4][j % 4] = y0 + y1;
                 }
             }
-        }
+            if (gated)
 #pragma unroll
-        for (int q = kTile - 4; q >= 0; q -= 4) {
-            float lb[4], dd[4];
+                for (int q = 0; q < kSub / 4; ++q) reduce4<LN>(ys[q], nl);
+            f2 dAs[2] = {0, 0};
 #pragma unroll
-            for (int j = q + 3; j >= q; --j) {
-                const float4 v = in[j * K::width];
-                const float4 B4 = *reinterpret_cast<const float4 *>(sB + j * K::NP);
-                const float4 C4 = *reinterpret_cast<const float4 *>(sC + j * K::NP);
-                const float Bk[4] = {B4.x, B4.y, B4.z, B4.w}, Ck[4] = {C4.x, C4.y, C4.z, C4.w};
+            for (int j = kSub - 1; j >= 0; --j) {
+                const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width], e = s.e[at + j * K::width];
+                f2 ql[2], qa[2];
                 float red[8];
-                lb[j - q] = dd[j - q] = 0.f;
 #pragma unroll
-                for (int k = 0; k < kNS; ++k) {
-                    const float lam = fmaf(v.z, Ck[k], w[k]);
-                    red[k] = v.z * H[j][k];
-                    red[4 + k] = v.y * lam;
-                    lb[j - q] = fmaf(lam, Bk[k], lb[j - q]);
-                    w[k] = E[j][k] * lam;
-                    const float pr = w[k] * (j ? H[j - 1][k] : hs[k]);
-                    dd[j - q] = fmaf(A2[k], pr, dd[j - q]);
-                    dA[k] = fmaf(v.x, pr, dA[k]);
+                for (int k = 0; k < 2; ++k) {
+                    const f2 lam = fma2(e, s.C[bt + (2 * j + k) * LN], w[k]);
+                    const f2 rc = mul2(e, H[j][k]), rb = mul2(u, lam);
+                    unpack2(rc, red[2 * k], red[2 * k + 1]);
+                    unpack2(rb, red[4 + 2 * k], red[5 + 2 * k]);
+                    ql[k] = mul2(lam, s.B[bt + (2 * j + k) * LN]);
+                    w[k] = mul2(E[j][k], lam);
+                    const f2 pr = mul2(w[k], j ? H[j - 1][k] : hs[k]);
+                    qa[k] = mul2(A2[k], pr);
+                    dAs[k] = fma2(d, pr, dAs[k]);
                 }
-                reduce_channels<LN>(red, lane, nl, s.red + (warp * kTile + j) * 2 * K::NP);
+                float v0, v1;
+                unpack2(add2(ql[0], ql[1]), v0, v1);
+                lb[j / 4][j % 4] = v0 + v1;
+                unpack2(add2(qa[0], qa[1]), v0, v1);
+                dd[j / 4][j % 4] = v0 + v1;
+                reduce_channels<LN>(red, lane);
+#pragma unroll
+                for (int i = 0; i < K::kept; ++i) sums[j][i] = red[i];
             }
-            reduce4<LN>(lb, nl);
-            reduce4<LN>(dd, nl);
-            if (LN <= 4 || nl < 4) {
+            dA[0] = add2(dA[0], dAs[0]);
+            dA[1] = add2(dA[1], dAs[1]);
 #pragma unroll
-                for (int j = 0; j < Kept<LN>::value; ++j) {
-                    const int at = (q + first_token<LN>(nl) + j) * K::width + ch;
-                    s.o[K::pairs + at] = lb[j];
-                    s.o[2 * K::pairs + at] = dd[j];
-                }
+            for (int q = 0; q < kSub / 4; ++q) {
+                reduce4<LN>(lb[q], nl);
+                reduce4<LN>(dd[q], nl);
+            }
+            if (LN <= 4 || nl < 4) {
+                float *o = s.o + (sub * kSub + first_token<LN>(nl)) * K::width + ch;
+#pragma unroll
+                for (int q = 0; q < kSub / 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < Kept<LN>::value; ++j) {
+                        if (gated) o[(4 * q + j) * K::width] = ys[q][j];
+                        o[K::pairs + (4 * q + j) * K::width] = lb[q][j];
+                        o[2 * K::pairs + (4 * q + j) * K::width] = dd[q][j];
+                    }
+            }
+            if (LN > 2 || lane < 8 * LN) {
+                // quantity v of the eight: dC for v < 4, dB from there on, state n0 + v % 4
+                const int v = where_reduced<LN>(lane);
+                float *r = s.red + (warp * kTile + sub * kSub) * 2 * K::NP + (v / 4) * K::NP + n0 + v % 4;
+#pragma unroll
+                for (int j = 0; j < kSub; ++j)
+#pragma unroll
+                    for (int i = 0; i < K::kept; ++i) r[j * 2 * K::NP + i] = sums[j][i];
             }
         }
-        if (tile > 0) stg.store(a, p, tb - kTile, n, s, buf ^ 1);
+        if (tile > 0) stg.store(tb - kTile, s, buf ^ 1);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < K::per; ++i) {
-            const int e = tid + i * K::threads, t = tb + e / K::width, cc = e % K::width;
-            if (t < t1 && cc < p.nc) {
-                const long long o = (row0 + t) * a.C + p.c0 + cc;
-                const float4 v = s.in[buf * K::pairs + e];
-                const float2 x2 = s.ex[buf * K::pairs + e];
-                const float q = s.o[K::pairs + e], Dc = a.D ? a.D[p.c0 + cc] : 0.f;
-                const float ddt = (fmaf(v.w, q, s.o[2 * K::pairs + e] * (1.f / kLog2e))) * x2.x;
+            const int t = tb + stg.t_first + i * Stager<T, LN, true>::t_step;
+            if (Stager<T, LN, true>::mine(i) && t < t1) {
+                const int e4 = tid + i * K::threads;
+                const ulonglong2 *own = reinterpret_cast<const ulonglong2 *>(s.own) + buf * 4 * K::quads + e4;
+                const ulonglong2 *o = reinterpret_cast<const ulonglong2 *>(s.o) + e4;
+                const ulonglong2 sig = own[0], dz = own[K::quads], d = own[2 * K::quads], g = own[3 * K::quads];
+                const ulonglong2 y = o[0], q = o[K::quads], ap = o[2 * K::quads];
+                const f2 sg2[2] = {sig.x, sig.y}, dz2[2] = {dz.x, dz.y}, d2[2] = {d.x, d.y}, g2[2] = {g.x, g.y};
+                const f2 y2[2] = {y.x, y.y}, q2[2] = {q.x, q.y}, ap2[2] = {ap.x, ap.y};
+                f2 x2[2];
+                kx[i].values(x2);
+                float ox[4], od[4], oz[4];
                 const bool in_seq = t < n;
-                ((T *)a.dx)[o] = from_f<T>(in_seq ? fmaf(v.x, q, Dc * v.z) : 0.f);
-                ((T *)a.ddt)[o] = from_f<T>(in_seq ? ddt : 0.f);
-                if (a.z) ((T *)a.dz)[o] = from_f<T>(in_seq ? x2.y * fmaf(Dc, v.w, s.o[e]) : 0.f);
-                if (in_seq) {
-                    dD = fmaf(v.z, v.w, dD);
-                    dbias += ddt;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f2 dx = fma2(d2[j], q2[j], mul2(Dc[j], g2[j]));
+                    f2 dt = mul2(fma2(x2[j], q2[j], mul2(ap2[j], both(1.f / kLog2e))), sg2[j]);
+                    f2 gz = mul2(dz2[j], fma2(Dc[j], x2[j], y2[j]));
+                    if (!in_seq) dx = dt = gz = 0;
+                    dD[j] = fma2(g2[j], x2[j], dD[j]);                    // 0 behind the end: g and x are
+                    dbias[j] = add2(dbias[j], dt);
+                    unpack2(dx, ox[2 * j], ox[2 * j + 1]);
+                    unpack2(dt, od[2 * j], od[2 * j + 1]);
+                    unpack2(gz, oz[2 * j], oz[2 * j + 1]);
                 }
+                const long long at = stg.x0 + (long long)tb * a.C + i * stg.xs;
+                store4((T *)a.dx + at, ox, stg.have, sg.vec);
+                store4((T *)a.ddt + at, od, stg.have, sg.vec);
+                if (gated) store4((T *)a.dz + at, oz, stg.have, sg.vec);
             }
         }
         for (int e = tid; e < kTile * 2 * K::NP; e += K::threads) {
@@ -410,36 +533,44 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                 for (int u = 0; u < K::warps; ++u) r += s.red[(u * kTile + j) * 2 * K::NP + m];
                 const long long plane = (long long)a.B * a.T * a.G * a.N;
                 const int ct = (p.c0 - p.g * (a.C / a.G)) / K::width;
-                sg.bc[(2 * (long long)ct + m / K::NP) * plane + ((row0 + t) * a.G + p.g) * a.N + st] = r;
+                sg.bc[(2 * (long long)ct + m / K::NP) * plane + (((long long)p.b * a.T + t) * a.G + p.g) * a.N + st] = r;
             }
         }
         __syncthreads();
     }
     // rows behind the sequence's end
-    for (long long e = (long long)count * kTile * K::width + tid; e < (long long)(t1 - t0) * K::width; e += K::threads) {
+    const long long row0 = (long long)p.b * a.T;
+    for (long long e = (long long)count * K::pairs + tid; e < (long long)(t1 - t0) * K::width; e += K::threads) {
         const int t = t0 + (int)(e / K::width), cc = (int)(e % K::width);
         if (cc < p.nc) {
             const long long o = (row0 + t) * a.C + p.c0 + cc;
             ((T *)a.dx)[o] = ((T *)a.ddt)[o] = from_f<T>(0.f);
-            if (a.z) ((T *)a.dz)[o] = from_f<T>(0.f);
+            if (gated) ((T *)a.dz)[o] = from_f<T>(0.f);
         }
     }
     // this block's parts of the sums over tokens
     const long long part = (long long)p.b * sg.segs + p.seg;
     if (live) {
-        store_states(sg.pA + (part * a.C + c) * a.N, n0, a.N, dA);
-        if (p.seg == 0 && a.dstate_out) store_states(a.dstate_out + ((long long)p.b * a.C + c) * a.N, n0, a.N, w);
+        float v[4];
+        unpack2(dA[0], v[0], v[1]);
+        unpack2(dA[1], v[2], v[3]);
+        store_states(sg.pA + (part * a.C + c) * a.N, n0, a.N, v);
+        unpack2(w[0], v[0], v[1]);
+        unpack2(w[1], v[2], v[3]);
+        if (p.seg == 0 && a.dstate_out) store_states(a.dstate_out + ((long long)p.b * a.C + c) * a.N, n0, a.N, v);
     }
-    // every thread's pairs were all of channel tid % width
-    s.o[tid] = dD;
-    s.o[K::threads + tid] = dbias;
+    // the threads' four channels, thread tid those from 4 (tid % row) on
+    float4 *end = reinterpret_cast<float4 *>(smem4);
+    reinterpret_cast<ulonglong2 *>(end)[tid] = make_ulonglong2(dD[0], dD[1]);
+    reinterpret_cast<ulonglong2 *>(end)[K::threads + tid] = make_ulonglong2(dbias[0], dbias[1]);
     __syncthreads();
     if (tid < p.nc) {
         float r0 = 0.f, r1 = 0.f;
+        const float *f = reinterpret_cast<const float *>(end);
 #pragma unroll
-        for (int i = 0; i < LN; ++i) {
-            r0 += s.o[i * K::width + tid];
-            r1 += s.o[K::threads + i * K::width + tid];
+        for (int i = 0; i < K::threads / (K::width / 4); ++i) {
+            r0 += f[i * K::width + tid];
+            r1 += f[4 * K::threads + i * K::width + tid];
         }
         sg.pD[part * a.C + p.c0 + tid] = r0;
         sg.pbias[part * a.C + p.c0 + tid] = r1;
@@ -512,7 +643,7 @@ size_t layout(int B, int T, int C, int G, int N, void *ws, Seg *sg) {
     sg->S = take(split ? parts * cn : 0);
     sg->R = take(split ? parts * cn : 0);
     sg->sum = take(split ? parts * C : 0);
-    sg->ckpt = take((size_t)B * ((T + kTile - 1) / kTile) * cn);
+    sg->ckpt = take((size_t)B * ((T + kSub - 1) / kSub) * cn);
     sg->bc = take(tiles * 2 * B * T * G * N);
     sg->pA = take(parts * cn);
     sg->pD = take(parts * C);
@@ -525,6 +656,8 @@ la_status bwd_ln(const ScanArgs &a, cudaStream_t st) {
     using K = Cfg<LN>;
     Seg sg;
     layout(a.B, a.T, a.C, a.G, a.N, a.ws, &sg);
+    sg.vec = quad_rows<T>(a.C / a.G, a.x, a.dt_in, a.z, a.dy, a.dx, a.ddt, a.dz);
+    sg.bvec = quad_rows<T>(a.N, a.Bm, a.Cm);
     const int tiles = (a.C / a.G + K::width - 1) / K::width;
     const dim3 grid((unsigned)((long long)a.B * sg.segs * a.G * tiles)), block(K::threads);
     la_status rc = LA_OK;
