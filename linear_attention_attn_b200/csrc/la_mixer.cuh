@@ -105,13 +105,12 @@ __device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
 // ----------------------------------------------------------- activations --
 // 1 / (1 + e^-x).  For x below about -88 the exponential overflows to infinity and the result
 // is 0; the relative error is a few 2^-22 where |x| is a few units.
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
 __device__ __forceinline__ f2 sigmoid2(f2 x) {
     float a, b;
-    unpack2(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
-    return pack2(rcp(a), rcp(b));
+    unpack2(x, a, b);
+    return pack2(sigmoid_f(a), sigmoid_f(b));
 }
-
-__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
 __device__ __forceinline__ float sigmoid(float x) { return sigmoid_f(x); }
 __device__ __forceinline__ f2 sigmoid(f2 x) { return sigmoid2(x); }
 

@@ -94,8 +94,8 @@ la_status check_scan(int B, int T, int C, int G, int N, la_dtype dt) {
     LA_TRY(check_btc(B, T, C, dt));
     if (G < 1 || C % G) return refuse(LA_ERR_INVALID_ARG, "C=%d is not a multiple of G=%d", C, G);
     if (N < 1 || N > 64) return refuse(LA_ERR_UNSUPPORTED, "N must be in [1, 64] (got %d)", N);
-    if ((double)B * T * G * N >= 274877906944.0 || (double)B * C * N >= 2147483648.0)
-        return refuse(LA_ERR_UNSUPPORTED, "tensor too large (B*T*G*N < 2^38, B*C*N < 2^31)");
+    if ((double)B * T * G * N >= 34359738368.0 || (double)B * C * N >= 2147483648.0)
+        return refuse(LA_ERR_UNSUPPORTED, "tensor too large (B*T*G*N < 2^35, B*C*N < 2^31)");
     return LA_OK;
 }
 

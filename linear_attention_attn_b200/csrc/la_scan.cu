@@ -33,7 +33,7 @@ template <int LN> struct Cfg {
     static constexpr int per = (quads + kThreads - 1) / kThreads;
     static constexpr int bquads = kTile * LN;               // 4 states of a token's B (or C)
     static constexpr int bper = (bquads + kThreads - 1) / kThreads;
-    static constexpr size_t smem = sizeof(f2) * (4 * pairs + 8 * kTile * LN) + sizeof(float) * 2 * pairs;
+    static constexpr size_t smem = sizeof(float) * (6 * pairs + 2 * 2 * kTile * kNS * LN);
 };
 
 struct Seg {
@@ -47,15 +47,12 @@ template <typename T, int LN, bool FULL>
 __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Place &p, int t0, int t1,
                                      const f2 (&A2)[2], f2 (&h)[2], float &sum, float *smem) {
     using K = Cfg<LN>;
-    // Every value that a pair of states shares is stored twice, side by side, and B and C in two
-    // planes of pairs, so that the inner loop reads 8 bytes a lane: such a read of at most 128
-    // different bytes a warp takes one pass through shared memory, a 16-byte one four.
-    f2 *s_d = reinterpret_cast<f2 *>(smem);                           // [2][kTile][width]: d, d
-    f2 *s_u = s_d + 2 * K::pairs;                                     // [2][kTile][width]: d x, d x
-    f2 *s_B = s_u + 2 * K::pairs;                                     // [2][kTile][2][LN]
-    f2 *s_C = s_B + 2 * kTile * 2 * LN;
-    float *s_y = reinterpret_cast<float *>(s_C + 2 * kTile * 2 * LN); // [2][kTile][width]
-    const int tid = threadIdx.x, nl = tid % LN, ch = tid / LN;
+    float *s_d = smem;                                                // [2][kTile][width]
+    float *s_u = s_d + 2 * K::pairs;                                  // [2][kTile][width]: d x
+    float *s_B = s_u + 2 * K::pairs;                                  // [2][kTile][4 LN]
+    float *s_C = s_B + 2 * kTile * kNS * LN;
+    float *s_y = s_C + 2 * kTile * kNS * LN;                          // [2][kTile][width]
+    const int tid = threadIdx.x, nl = lane_states<LN>(), ch = lane_channel<LN>();
     const int n = min(seq_end(a.lengths, p.b, a.T), t1);              // tokens that exist
     const int tiles = n > t0 ? (n - t0 + kTile - 1) / kTile : 0;
     const long long row0 = (long long)p.b * a.T + t0;
@@ -113,27 +110,21 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
                     d[j] = add2(d[j], bias[j]);
                     if (a.softplus) d[j] = softplus2(d[j]);
                     if (t_first + i * t_step >= left) d[j] = 0;       // behind the end: the state stays
-                    const f2 u = mul2(d[j], x[j]);
-                    float v0, v1, w0, w1;
-                    unpack2(d[j], v0, v1);
-                    unpack2(u, w0, w1);
-                    const int at = buf * K::pairs + 4 * (tid + i * kThreads) + 2 * j;
-                    *reinterpret_cast<ulonglong2 *>(s_d + at) = make_ulonglong2(both(v0), both(v1));
-                    *reinterpret_cast<ulonglong2 *>(s_u + at) = make_ulonglong2(both(w0), both(w1));
                 }
+                const int at = buf * K::quads + tid + i * kThreads;
+                reinterpret_cast<ulonglong2 *>(s_d)[at] = make_ulonglong2(d[0], d[1]);
+                reinterpret_cast<ulonglong2 *>(s_u)[at] = make_ulonglong2(mul2(d[0], x[0]), mul2(d[1], x[1]));
             }
 #pragma unroll
         for (int i = 0; i < K::bper; ++i)
             if (K::bquads % kThreads == 0 || tid + i * kThreads < K::bquads) {
                 f2 v[2];
-                const int at = (buf * kTile + b_first + i * b_step) * 2 * LN + tid % LN;
+                const int at = buf * K::bquads + tid + i * kThreads;
                 rB[i].values(v);
-                s_B[at] = v[0];
-                s_B[at + LN] = v[1];
+                reinterpret_cast<ulonglong2 *>(s_B)[at] = make_ulonglong2(v[0], v[1]);
                 if (FULL) {
                     rC[i].values(v);
-                    s_C[at] = v[0];
-                    s_C[at + LN] = v[1];
+                    reinterpret_cast<ulonglong2 *>(s_C)[at] = make_ulonglong2(v[0], v[1]);
                 }
             }
     };
@@ -151,8 +142,9 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
             kz[i] = rz[i];
         }
         if (tile + 1 < tiles) load(tile + 1);
-        const f2 *pd = s_d + buf * K::pairs + ch, *pu = s_u + buf * K::pairs + ch;
-        const f2 *pB = s_B + buf * kTile * 2 * LN + nl, *pC = s_C + buf * kTile * 2 * LN + nl;
+        const float *pd = s_d + buf * K::pairs + ch, *pu = s_u + buf * K::pairs + ch;
+        const ulonglong2 *pB = reinterpret_cast<const ulonglong2 *>(s_B) + buf * K::bquads + nl;
+        const ulonglong2 *pC = reinterpret_cast<const ulonglong2 *>(s_C) + buf * K::bquads + nl;
         // the sums stay in registers until the tile is done: a store to shared memory in between would
         // keep the next tokens' loads from moving up
         float ys[kTile / 4][4];
@@ -160,18 +152,18 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
         for (int q = 0; q < kTile; q += 4) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f2 d = pd[(q + j) * K::width], u = pu[(q + j) * K::width];
-                const f2 *B = pB + (q + j) * 2 * LN, *C = pC + (q + j) * 2 * LN;
-                h[0] = fma2(ex2_2(mul2(d, A2[0])), h[0], mul2(u, B[0]));
-                h[1] = fma2(ex2_2(mul2(d, A2[1])), h[1], mul2(u, B[LN]));
+                const float d1 = pd[(q + j) * K::width];
+                const f2 d = both(d1), u = both(pu[(q + j) * K::width]);
+                const ulonglong2 B = pB[(q + j) * LN];
+                h[0] = fma2(ex2_2(mul2(d, A2[0])), h[0], mul2(u, B.x));
+                h[1] = fma2(ex2_2(mul2(d, A2[1])), h[1], mul2(u, B.y));
                 if (FULL) {
+                    const ulonglong2 C = pC[(q + j) * LN];
                     float y0, y1;
-                    unpack2(fma2(C[0], h[0], mul2(C[LN], h[1])), y0, y1);
+                    unpack2(fma2(C.x, h[0], mul2(C.y, h[1])), y0, y1);
                     ys[q / 4][j] = y0 + y1;
                 } else {
-                    float d0, d1;
-                    unpack2(d, d0, d1);
-                    sum += d0;
+                    sum += d1;
                 }
             }
             if (FULL) reduce4<LN>(ys[q / 4], nl);
@@ -225,7 +217,7 @@ scan_fwd_kernel(ScanArgs a, Seg sg, int tiles) {
     float *smem = reinterpret_cast<float *>(smem4);
     Place p = place(blockIdx.x, a.G, a.C / a.G, tiles, PASS == 0 ? 1 : sg.segs - 1, K::width);
     if (PASS == 2) p.seg += 1;
-    const int nl = threadIdx.x % LN, ch = threadIdx.x / LN, n0 = nl * kNS;
+    const int nl = lane_states<LN>(), ch = lane_channel<LN>(), n0 = nl * kNS;
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
     float A4[kNS] = {}, h4[kNS] = {};

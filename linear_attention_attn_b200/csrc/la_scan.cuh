@@ -1,8 +1,11 @@
 // la_scan.cuh -- layout shared by the forward, step and backward kernels of the selective scan.
 //
-// A channel's N states are spread over LN neighbouring lanes of a warp, kNS = 4 each (N is padded
-// to 4 LN with rates and projections of zero, which contribute nothing), so sums over n are
-// log2(LN) shuffles and a warp works on 32 / LN channels.
+// A channel's N states are spread over LN lanes of a warp, kNS = 4 each (N is padded to 4 LN with
+// rates and projections of zero, which contribute nothing), so sums over n are log2(LN) shuffles and
+// a warp works on S = 32 / LN channels.  Lane l has states 4 (l / S) on of channel l % S: lanes that
+// read the same B and C are neighbours, and a 16-byte read of shared memory whose neighbours agree
+// takes 2 passes instead of 4 (measured; 8 bytes: 1 instead of 2), while the reads that differ from
+// channel to channel are single floats, which take 1 whatever they differ by.
 #pragma once
 
 #include "la_mixer.cuh"
@@ -13,42 +16,42 @@ namespace scan {
 constexpr int kNS = 4;             // states a lane holds
 constexpr int kTile = 16;          // tokens staged in shared memory at a time
 
-// e^-|r| of a pair (0 from 128 on) with the argument's rounding repaired: r log2(e) as a product
-// and its remainder, and the part of log2(e) that one float leaves out.
-__device__ __forceinline__ f2 exp_neg_abs(f2 r) {
+// e^-|r| (0 from 128 on) with the argument's rounding repaired: r log2(e) as a product and its
+// remainder, and the part of log2(e) that one float leaves out.  (One value at a time: a packed
+// operation takes no constant operand, and keeping all of these in register pairs costs more.)
+__device__ __forceinline__ float exp_neg_abs(float r) {
     constexpr float rest = (float)(1.44269504088896340736 - (double)kLog2e);
-    float a, b;
-    unpack2(r, a, b);
-    const f2 m = pack2(fmaxf(-fabsf(a), -128.f), fmaxf(-fabsf(b), -128.f)), v = mul2(m, both(kLog2e));
-    const f2 lo = fma2(m, both(rest), fma2(m, both(kLog2e), mul2(v, both(-1.f))));
-    const f2 e = ex2_2(v);
-    return fma2(e, mul2(lo, both(0.69314718055994531f)), e);
+    const float m = fmaxf(-fabsf(r), -128.f), v = m * kLog2e;
+    const float lo = fmaf(m, rest, fmaf(m, kLog2e, -v)), e = ex2(v);
+    return fmaf(e, lo * 0.69314718055994531f, e);
 }
 // log(1 + e^r) = max(r, 0) + log1p(e), e = e^-|r| in (0, 1]: log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
-// by atanh's series up to s^13 (the next term is below 2^-26 of the sum).  A NaN stays one.
-__device__ __forceinline__ f2 softplus_from(f2 r, f2 e) {
-    float a, b, c, d;
-    unpack2(add2(e, both(2.f)), a, b);
-    const f2 s = mul2(e, pack2(rcp(a), rcp(b))), q = mul2(s, s);
-    f2 p = fma2(q, both(1.f / 13.f), both(1.f / 11.f));
-    p = fma2(q, p, both(1.f / 9.f));
-    p = fma2(q, p, both(1.f / 7.f));
-    p = fma2(q, p, both(1.f / 5.f));
-    p = fma2(q, p, both(1.f / 3.f));
-    p = fma2(q, p, both(1.f));
-    unpack2(r, a, b);
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(c) : "f"(a));
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(d) : "f"(b));
-    return fma2(add2(s, s), p, pack2(c, d));
+// with atanh(s) / s a polynomial in s^2, fitted through the Chebyshev points of [0, 1/9] (its error is
+// below 2^-25).  A NaN stays one.
+__device__ __forceinline__ float softplus_from(float r, float e) {
+    const float s = e * rcp(2.f + e), q = s * s;
+    float p = fmaf(q, 0.1342574900842183f, 0.1411830990323794f), top;
+    p = fmaf(q, p, 0.200037803224282f);
+    p = fmaf(q, p, 0.3333332016834966f);
+    p = fmaf(q, p, 1.f);
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(top) : "f"(r));
+    return fmaf(s + s, p, top);
 }
-__device__ __forceinline__ f2 softplus2(f2 r) { return softplus_from(r, exp_neg_abs(r)); }
-__device__ __forceinline__ float softplus_f(float r) {
+__device__ __forceinline__ float softplus_f(float r) { return softplus_from(r, exp_neg_abs(r)); }
+__device__ __forceinline__ f2 softplus2(f2 r) {
     float a, b;
-    unpack2(softplus2(both(r)), a, b);
-    return a;
+    unpack2(r, a, b);
+    return pack2(softplus_f(a), softplus_f(b));
 }
+
 __device__ __forceinline__ int seq_end(const int *lengths, int b, int T) {
     return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+// The quarter (of 4 states) that this thread has, and its channel in the block's tile.
+template <int LN> __device__ __forceinline__ int lane_states() { return (threadIdx.x & 31) / (32 / LN); }
+template <int LN> __device__ __forceinline__ int lane_channel() {
+    return (threadIdx.x >> 5) * (32 / LN) + (threadIdx.x & 31) % (32 / LN);
 }
 
 // Sums v[0..3] (four tokens) over the LN lanes of a channel.  Each step hands half of the values
@@ -61,19 +64,20 @@ __device__ __forceinline__ int first_token(int nl) {
 }
 template <int LN>
 __device__ __forceinline__ void reduce4(float (&v)[4], int nl) {
+    constexpr int S = 32 / LN;
     if (LN >= 2) {
         const bool hi = nl & 1;
         const float s0 = hi ? v[0] : v[2], s1 = hi ? v[1] : v[3];
-        v[0] = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, s0, 1);
-        v[1] = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, s1, 1);
+        v[0] = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, s0, S);
+        v[1] = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, s1, S);
     }
     if (LN >= 4) {
         const bool hi = nl & 2;
         const float s = hi ? v[0] : v[1];
-        v[0] = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, s, 2);
+        v[0] = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, s, 2 * S);
     }
-    if (LN >= 8) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);
-    if (LN >= 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
+    if (LN >= 8) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4 * S);
+    if (LN >= 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8 * S);
 }
 
 // Where a block works: batch entry, segment of the sequence, and a tile of channels of one group.

@@ -32,7 +32,7 @@ using namespace scan;
 constexpr int kSub = 8;            // tokens whose states and decays are in registers at a time
 
 template <int LN> struct Cfg {
-    static constexpr int threads = LN == 1 ? 128 : 256;
+    static constexpr int threads = LN == 1 ? 64 : 128;
     static constexpr int warps = threads / 32;
     static constexpr int width = threads / LN;
     static constexpr int NP = kNS * LN;
@@ -41,40 +41,56 @@ template <int LN> struct Cfg {
     static constexpr int per = (quads + threads - 1) / threads;
     static constexpr int bquads = kTile * LN;
     static constexpr int bper = (bquads + threads - 1) / threads;
-    static constexpr int kept = LN >= 16 ? 4 : LN == 8 ? 2 : 1;   // sums over channels that a lane ends up with
-    // planes d, u, e (pairs, twice), B and C (pairs, twice), the quads' own (four floats, twice), the
-    // three sums over states, the warps' sums of dC and dB
-    static constexpr size_t smem = sizeof(f2) * (6 * pairs + 8 * kTile * LN) +
-                                   sizeof(float) * (8 * pairs + 3 * pairs + warps * kTile * 2 * NP);
+    static constexpr int subs = kTile / kSub;
+    // d, u, e, sigma, dz (twice), B and C (twice), the three sums over states, the warps' sums of dC
+    // and dB, and their places for forming them; the lanes' states before sub-tiles (twice)
+    static constexpr size_t smem = sizeof(float) * (10 * pairs + 4 * kTile * NP + 3 * pairs + warps * kTile * 2 * NP) +
+                                   warps * kSub * 2 * (512 + 16 * LN) + 2 * subs * threads * 16;
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
 };
 
 struct Seg {
     int segs, len;
     float *S, *R, *sum;            // [B, segs, C, N] twice, [B, segs, C]
-    float *ckpt;                   // [B, ceil(T / kSub), C, N]
+    float *ckpt;                   // [B, ceil(T / kSub), C, 4 LN]
     float *bc;                     // [tiles][2][B T G N]: the channel tiles' parts of dC and dB
     float *pA, *pD, *pbias;        // [B segs][C N], [B segs][C] twice
     int vec, bvec;                 // rows of the [B,T,C] tensors (of Bm, Cm) allow accesses of 4 elements
 };
 
+// The sums over a warp's 32 / LN channels of what its lanes hold for dC and dB of kSub tokens, four
+// states each: every lane leaves them in the warp's part of shared memory, then adds up whole columns.
+// (Exchanging halves by shuffles takes 28 instructions a token for these sums; this takes 9.)
+// A quarter's lanes are followed by 16 bytes of room, so that reads of different quarters and rows
+// meet different banks.
+template <int LN> struct Columns {
+    static constexpr int quarter = 512 / LN + 16;                  // bytes from one quarter's lanes to the next
+    static constexpr int stride = LN * quarter;                    // bytes from one (token, quantity) to the next
+    static constexpr int bytes = kSub * 2 * stride;                // a warp
+    static constexpr int items = kSub * 2 * LN;                    // columns of four states
+};
 template <int LN>
 struct Smem {
     using K = Cfg<LN>;
-    // As in the forward, what a pair of states shares lies twice side by side, B and C in two planes.
-    f2 *d, *u, *e;                 // [2][kTile][width]
-    f2 *B, *C;                     // [2][kTile][2][LN]
-    float4 *own;                   // [2][4][quads]: sigma(dt + bias) (1 without softplus), dy silu'(z), d, e
+    float *d, *u, *e;              // [2][kTile][width]
+    float *sig, *dz;               // [2][kTile][width]: sigma(dt + bias) (1 without softplus), dy silu'(z)
+    float *B, *C;                  // [2][kTile][NP]
     float *o;                      // [3][kTile][width]: sum_n C h, q, sum_n A p (in units of 1 / log2 e)
     float *red;                    // [warps][kTile][2][NP]
+    char *columns;                 // [warps], see sum_channels
+    float4 *before;                // [2][kTile / kSub][threads]
     __device__ explicit Smem(float *p) {
-        own = reinterpret_cast<float4 *>(p);
-        d = reinterpret_cast<f2 *>(p + 8 * K::pairs);
+        d = p;
         u = d + 2 * K::pairs;
         e = u + 2 * K::pairs;
-        B = e + 2 * K::pairs;
-        C = B + 4 * kTile * LN;
-        o = reinterpret_cast<float *>(C + 4 * kTile * LN);
+        sig = e + 2 * K::pairs;
+        dz = sig + 2 * K::pairs;
+        B = dz + 2 * K::pairs;
+        C = B + 2 * kTile * K::NP;
+        o = C + 2 * kTile * K::NP;
         red = o + 3 * K::pairs;
+        columns = reinterpret_cast<char *>(red + K::warps * kTile * 2 * K::NP);
+        before = reinterpret_cast<float4 *>(columns + K::warps * Columns<LN>::bytes);
     }
 };
 
@@ -134,39 +150,34 @@ struct Stager {
                 if (BACK) rC[i].load((const T *)a.Cm + bo + i * bs, live, sg.bvec);
             }
     }
-    static __device__ __forceinline__ void twice(f2 *plane, int at, f2 v) {
-        float x, y;
-        unpack2(v, x, y);
-        *reinterpret_cast<ulonglong2 *>(plane + at) = make_ulonglong2(both(x), both(y));
+    static __device__ __forceinline__ void put(float *plane, int at, const f2 (&v)[2]) {
+        reinterpret_cast<ulonglong2 *>(plane)[at] = make_ulonglong2(v[0], v[1]);
     }
     __device__ __forceinline__ void store(int tb, Smem<LN> &s, int buf) {
 #pragma unroll
         for (int i = 0; i < K::per; ++i)
             if (mine(i)) {
-                const int at = threadIdx.x + i * K::threads;
+                const int at = buf * K::quads + threadIdx.x + i * K::threads;
                 const bool gone = tb + t_first + i * t_step >= n;         // behind the end: the state stays
-                f2 d[2], x[2], sig[2] = {both(1.f), both(1.f)};
+                f2 d[2], x[2], u[2], sig[2] = {both(1.f), both(1.f)};
                 rd[i].values(d);
                 rx[i].values(x);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     d[j] = add2(d[j], bias[j]);
                     if (a.softplus) {
-                        const f2 e = exp_neg_abs(d[j]);
-                        if (BACK) {
-                            // sigma(r): 1 / (1 + e) for r >= 0, e / (1 + e) below
-                            float r0, r1, e0, e1, q0, q1;
-                            unpack2(d[j], r0, r1);
-                            unpack2(e, e0, e1);
-                            unpack2(add2(e, both(1.f)), q0, q1);
-                            sig[j] = pack2((r0 < 0.f ? e0 : 1.f) * rcp(q0), (r1 < 0.f ? e1 : 1.f) * rcp(q1));
-                        }
-                        d[j] = softplus_from(d[j], e);
+                        float r0, r1;
+                        unpack2(d[j], r0, r1);
+                        const float e0 = exp_neg_abs(r0), e1 = exp_neg_abs(r1);
+                        // sigma(r): 1 / (1 + e) for r >= 0, e / (1 + e) below
+                        if (BACK) sig[j] = pack2((r0 < 0.f ? e0 : 1.f) * rcp(1.f + e0), (r1 < 0.f ? e1 : 1.f) * rcp(1.f + e1));
+                        d[j] = pack2(softplus_from(r0, e0), softplus_from(r1, e1));
                     }
                     if (gone) d[j] = 0;
-                    twice(s.d, buf * K::pairs + 4 * at + 2 * j, d[j]);
-                    twice(s.u, buf * K::pairs + 4 * at + 2 * j, mul2(d[j], x[j]));
+                    u[j] = mul2(d[j], x[j]);
                 }
+                put(s.d, at, d);
+                put(s.u, at, u);
                 if (BACK) {
                     f2 g[2], z[2], dz[2] = {0, 0};
                     rg[i].values(g);
@@ -180,65 +191,65 @@ struct Stager {
                             g[j] = mul2(gs, z[j]);
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) twice(s.e, buf * K::pairs + 4 * at + 2 * j, g[j]);
-                    ulonglong2 *own = reinterpret_cast<ulonglong2 *>(s.own) + buf * 4 * K::quads + at;
-                    own[0] = make_ulonglong2(sig[0], sig[1]);
-                    own[K::quads] = make_ulonglong2(dz[0], dz[1]);
-                    own[2 * K::quads] = make_ulonglong2(d[0], d[1]);
-                    own[3 * K::quads] = make_ulonglong2(g[0], g[1]);
+                    put(s.e, at, g);
+                    put(s.sig, at, sig);
+                    put(s.dz, at, dz);
                 }
             }
 #pragma unroll
         for (int i = 0; i < K::bper; ++i)
             if (mine_b(i)) {
                 f2 v[2];
-                const int at = (buf * kTile + b_first + i * b_step) * 2 * LN + threadIdx.x % LN;
+                const int at = buf * K::bquads + threadIdx.x + i * K::threads;
                 rB[i].values(v);
-                s.B[at] = v[0];
-                s.B[at + LN] = v[1];
+                put(s.B, at, v);
                 if (BACK) {
                     rC[i].values(v);
-                    s.C[at] = v[0];
-                    s.C[at + LN] = v[1];
+                    put(s.C, at, v);
                 }
             }
     }
 };
 
-// Sums v[0..7] over the 32 / LN channels of a warp (lanes of equal nl): each step hands half of the
-// values to the partner.  Afterwards a lane's first Cfg::kept values are sums of the quantities
-// from where_reduced() on, for the states of its nl.
 template <int LN>
-__device__ __forceinline__ void reduce_channels(float (&v)[8], int lane) {
-    {
-        const bool hi = lane & LN;
+__device__ __forceinline__ void sum_channels(const f2 (&rc)[kSub][2], const f2 (&rb)[kSub][2], char *mine, int lane,
+                                             float *out) {
+    typedef Columns<LN> Q;
+    constexpr int NP = kNS * LN;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float s = hi ? v[i] : v[i + 4];
-            v[i] = (hi ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, s, LN);
+    for (int j = 0; j < kSub; ++j) {
+        char *p = mine + 2 * j * Q::stride + lane / (32 / LN) * Q::quarter + lane % (32 / LN) * 16;
+        *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(rc[j][0], rc[j][1]);
+        *reinterpret_cast<ulonglong2 *>(p + Q::stride) = make_ulonglong2(rb[j][0], rb[j][1]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < Q::items; i += 32) {
+        const int it = i + lane, row = it / LN, nl = it % LN;
+        if (Q::items % 32 == 0 || it < Q::items) {
+            f2 s0 = 0, s1 = 0;
+#pragma unroll
+            for (int ch = 0; ch < 32 / LN; ++ch) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(mine + row * Q::stride + nl * Q::quarter + ch * 16);
+                s0 = ch ? add2(s0, v.x) : v.x;
+                s1 = ch ? add2(s1, v.y) : v.y;
+            }
+            // row = 2 token + quantity: out is [token][quantity][NP]
+            *reinterpret_cast<ulonglong2 *>(out + row * NP + nl * kNS) = make_ulonglong2(s0, s1);
         }
     }
-    if (LN <= 8) {
-        const bool hi = lane & (2 * LN);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float s = hi ? v[i] : v[i + 2];
-            v[i] = (hi ? v[i + 2] : v[i]) + __shfl_xor_sync(0xffffffffu, s, 2 * LN);
-        }
-    }
-    if (LN <= 4) {
-        const bool hi = lane & (4 * LN);
-        const float s = hi ? v[0] : v[1];
-        v[0] = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, s, 4 * LN);
-    }
-    if (LN <= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8 * LN);
-    if (LN <= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16 * LN);
+    __syncwarp();
 }
-template <int LN>
-__device__ __forceinline__ int where_reduced(int lane) {
-    return (lane & LN ? 4 : 0) + (LN <= 8 && lane & (2 * LN) ? 2 : 0) + (LN <= 4 && lane & (4 * LN) ? 1 : 0);
-}
+
+// Four states' B or C of a token.
+struct Four {
+    f2 v[2];
+    __device__ __forceinline__ explicit Four(const float *p) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(p);
+        v[0] = q.x;
+        v[1] = q.y;
+    }
+};
 
 // First launch of the segmented form: (S, R, sum of d) of every segment.
 template <typename T, int LN>
@@ -248,7 +259,7 @@ scan_bwd_ends(ScanArgs a, Seg sg, int tiles) {
     extern __shared__ float4 smem4[];
     Smem<LN> s(reinterpret_cast<float *>(smem4));
     const Place p = place(blockIdx.x, a.G, a.C / a.G, tiles, sg.segs, K::width);
-    const int nl = threadIdx.x % LN, ch = threadIdx.x / LN, n0 = nl * kNS;
+    const int nl = lane_states<LN>(), ch = lane_channel<LN>(), n0 = nl * kNS;
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
     float A4[kNS] = {}, sum = 0.f;
@@ -266,19 +277,19 @@ scan_bwd_ends(ScanArgs a, Seg sg, int tiles) {
         __syncthreads();
         const int buf = tile & 1;
         if (tile + 1 < count) stg.load(t0 + (tile + 1) * kTile);
-        const int at = buf * K::pairs + ch, bt = buf * kTile * 2 * LN + nl;
+        const int at = buf * K::pairs + ch, bt = buf * kTile * K::NP + n0;
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
-            const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width], e = s.e[at + j * K::width];
-            float d0, d1;
-            unpack2(d, d0, d1);
-            sum += d0;
+            const float d1 = s.d[at + j * K::width];
+            const f2 d = both(d1), u = both(s.u[at + j * K::width]), e = both(s.e[at + j * K::width]);
+            const Four B(s.B + bt + j * K::NP), C(s.C + bt + j * K::NP);
+            sum += d1;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const f2 E = ex2_2(mul2(d, A2[k]));
-                h[k] = fma2(E, h[k], mul2(u, s.B[bt + (2 * j + k) * LN]));
+                h[k] = fma2(E, h[k], mul2(u, B.v[k]));
                 P[k] = mul2(P[k], E);
-                R[k] = fma2(P[k], mul2(e, s.C[bt + (2 * j + k) * LN]), R[k]);
+                R[k] = fma2(P[k], mul2(e, C.v[k]), R[k]);
             }
         }
         if (tile + 1 < count) stg.store(t0 + (tile + 1) * kTile, s, buf ^ 1);
@@ -303,7 +314,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
     Smem<LN> s(reinterpret_cast<float *>(smem4));
     const Place p = place(blockIdx.x, a.G, a.C / a.G, tiles, sg.segs, K::width);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nl = tid % LN, ch = tid / LN, n0 = nl * kNS;
+    const int nl = lane_states<LN>(), ch = lane_channel<LN>(), n0 = nl * kNS;
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
     f2 A2[2], h[2], w[2];
@@ -346,8 +357,8 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
     const int count = n > t0 ? (n - t0 + kTile - 1) / kTile : 0;
     const long long subs_t = (a.T + kSub - 1) / kSub;
     // this lane's states before sub-tile i of the segment
-    float *ck = sg.ckpt + (((long long)p.b * subs_t + t0 / kSub) * a.C + c) * a.N;
-    const long long ck_step = (long long)a.C * a.N;
+    float *ck = sg.ckpt + (((long long)p.b * subs_t + t0 / kSub) * a.C + c) * K::NP + n0;
+    const long long ck_step = (long long)a.C * K::NP;
     const int subs = count > 0 ? (n - t0 + kSub - 1) / kSub : 0;
 
     // ---- forwards: the state before every sub-tile
@@ -361,25 +372,23 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
             __syncthreads();
             const int buf = tile & 1;
             if (tile + 1 < count) stg.load(t0 + (tile + 1) * kTile);
-            const int at = buf * K::pairs + ch, bt = buf * kTile * 2 * LN + nl;
+            const int at = buf * K::pairs + ch, bt = buf * kTile * K::NP + n0;
             f2 mid[kTile / kSub][2];
 #pragma unroll
             for (int j = 0; j < kTile; ++j) {
-                const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width];
+                const f2 d = both(s.d[at + j * K::width]), u = both(s.u[at + j * K::width]);
+                const Four B(s.B + bt + j * K::NP);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (j % kSub == 0) mid[j / kSub][k] = h[k];
-                    h[k] = fma2(ex2_2(mul2(d, A2[k])), h[k], mul2(u, s.B[bt + (2 * j + k) * LN]));
+                    h[k] = fma2(ex2_2(mul2(d, A2[k])), h[k], mul2(u, B.v[k]));
                 }
             }
 #pragma unroll
             for (int i = 0; i < kTile / kSub; ++i)
-                if (live && tile * (kTile / kSub) + i < subs) {
-                    float v[4];
-                    unpack2(mid[i][0], v[0], v[1]);
-                    unpack2(mid[i][1], v[2], v[3]);
-                    store_states(ck + (tile * (kTile / kSub) + i) * ck_step, n0, a.N, v);
-                }
+                if (live && tile * K::subs + i < subs)
+                    *reinterpret_cast<ulonglong2 *>(ck + (tile * K::subs + i) * ck_step) =
+                        make_ulonglong2(mid[i][0], mid[i][1]);
             if (tile + 1 < count) stg.store(t0 + (tile + 1) * kTile, s, buf ^ 1);
         }
         __syncthreads();
@@ -396,39 +405,50 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
         Dc[0] = pack2(v[0], v[1]);
         Dc[1] = pack2(v[2], v[3]);
     }
+    // the states before a tile's sub-tiles come a tile ahead, each lane's into its own place
+    auto fetch = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < K::subs; ++i)
+            copy_async<16>(s.before + ((tile & 1) * K::subs + i) * K::threads + tid,
+                           ck + (long long)(tile * K::subs + i) * ck_step, live && tile * K::subs + i < subs);
+        copy_commit();
+    };
     if (count > 0) {
+        fetch(count - 1);
         stg.load(t0 + (count - 1) * kTile);
         stg.store(t0 + (count - 1) * kTile, s, (count - 1) & 1);
     }
     __syncthreads();
     for (int tile = count - 1; tile >= 0; --tile) {
         const int buf = tile & 1, tb = t0 + tile * kTile;
-        float hs4[kTile / kSub][kNS] = {};
-#pragma unroll
-        for (int i = 0; i < kTile / kSub; ++i)
-            if (live && tile * (kTile / kSub) + i < subs)
-                load_states(ck + (tile * (kTile / kSub) + i) * ck_step, n0, a.N, hs4[i]);
+        copy_wait<0>();
+        if (tile > 0) fetch(tile - 1);
         Quad<T> kx[K::per];                                   // this tile's x, for its outputs
 #pragma unroll
         for (int i = 0; i < K::per; ++i) kx[i] = stg.rx[i];
         if (tile > 0) stg.load(tb - kTile);
 #pragma unroll
         for (int sub = kTile / kSub - 1; sub >= 0; --sub) {
-            const int at = buf * K::pairs + sub * kSub * K::width + ch, bt = (buf * kTile + sub * kSub) * 2 * LN + nl;
-            const f2 hs[2] = {pack2(hs4[sub][0], hs4[sub][1]), pack2(hs4[sub][2], hs4[sub][3])};
+            const int at = buf * K::pairs + sub * kSub * K::width + ch, bt = (buf * kTile + sub * kSub) * K::NP + n0;
+            const ulonglong2 before =
+                *reinterpret_cast<const ulonglong2 *>(s.before + (buf * K::subs + sub) * K::threads + tid);
+            const f2 hs[2] = {before.x, before.y};
             f2 H[kSub][2], E[kSub][2];
-            float ys[kSub / 4][4], lb[kSub / 4][4], dd[kSub / 4][4], sums[kSub][K::kept];
+            float ys[kSub / 4][4], lb[kSub / 4][4], dd[kSub / 4][4];
+            f2 rc[kSub][2], rb[kSub][2];
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
-                const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width];
+                const f2 d = both(s.d[at + j * K::width]), u = both(s.u[at + j * K::width]);
+                const Four B(s.B + bt + j * K::NP);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     E[j][k] = ex2_2(mul2(d, A2[k]));
-                    H[j][k] = fma2(E[j][k], j ? H[j - 1][k] : hs[k], mul2(u, s.B[bt + (2 * j + k) * LN]));
+                    H[j][k] = fma2(E[j][k], j ? H[j - 1][k] : hs[k], mul2(u, B.v[k]));
                 }
                 if (gated) {
+                    const Four C(s.C + bt + j * K::NP);
                     float y0, y1;
-                    unpack2(fma2(s.C[bt + 2 * j * LN], H[j][0], mul2(s.C[bt + (2 * j + 1) * LN], H[j][1])), y0, y1);
+                    unpack2(fma2(C.v[0], H[j][0], mul2(C.v[1], H[j][1])), y0, y1);
                     ys[j / 4][j % 4] = y0 + y1;
                 }
             }
@@ -438,16 +458,16 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
             f2 dAs[2] = {0, 0};
 #pragma unroll
             for (int j = kSub - 1; j >= 0; --j) {
-                const f2 d = s.d[at + j * K::width], u = s.u[at + j * K::width], e = s.e[at + j * K::width];
+                const f2 d = both(s.d[at + j * K::width]), u = both(s.u[at + j * K::width]),
+                         e = both(s.e[at + j * K::width]);
+                const Four B(s.B + bt + j * K::NP), C(s.C + bt + j * K::NP);
                 f2 ql[2], qa[2];
-                float red[8];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const f2 lam = fma2(e, s.C[bt + (2 * j + k) * LN], w[k]);
-                    const f2 rc = mul2(e, H[j][k]), rb = mul2(u, lam);
-                    unpack2(rc, red[2 * k], red[2 * k + 1]);
-                    unpack2(rb, red[4 + 2 * k], red[5 + 2 * k]);
-                    ql[k] = mul2(lam, s.B[bt + (2 * j + k) * LN]);
+                    const f2 lam = fma2(e, C.v[k], w[k]);
+                    rc[j][k] = mul2(e, H[j][k]);
+                    rb[j][k] = mul2(u, lam);
+                    ql[k] = mul2(lam, B.v[k]);
                     w[k] = mul2(E[j][k], lam);
                     const f2 pr = mul2(w[k], j ? H[j - 1][k] : hs[k]);
                     qa[k] = mul2(A2[k], pr);
@@ -458,9 +478,6 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                 lb[j / 4][j % 4] = v0 + v1;
                 unpack2(add2(qa[0], qa[1]), v0, v1);
                 dd[j / 4][j % 4] = v0 + v1;
-                reduce_channels<LN>(red, lane);
-#pragma unroll
-                for (int i = 0; i < K::kept; ++i) sums[j][i] = red[i];
             }
             dA[0] = add2(dA[0], dAs[0]);
             dA[1] = add2(dA[1], dAs[1]);
@@ -480,15 +497,8 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                         o[2 * K::pairs + (4 * q + j) * K::width] = dd[q][j];
                     }
             }
-            if (LN > 2 || lane < 8 * LN) {
-                // quantity v of the eight: dC for v < 4, dB from there on, state n0 + v % 4
-                const int v = where_reduced<LN>(lane);
-                float *r = s.red + (warp * kTile + sub * kSub) * 2 * K::NP + (v / 4) * K::NP + n0 + v % 4;
-#pragma unroll
-                for (int j = 0; j < kSub; ++j)
-#pragma unroll
-                    for (int i = 0; i < K::kept; ++i) r[j * 2 * K::NP + i] = sums[j][i];
-            }
+            sum_channels<LN>(rc, rb, s.columns + warp * Columns<LN>::bytes, lane,
+                             s.red + (warp * kTile + sub * kSub) * 2 * K::NP);
         }
         if (tile > 0) stg.store(tb - kTile, s, buf ^ 1);
         __syncthreads();
@@ -497,10 +507,10 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
             const int t = tb + stg.t_first + i * Stager<T, LN, true>::t_step;
             if (Stager<T, LN, true>::mine(i) && t < t1) {
                 const int e4 = tid + i * K::threads;
-                const ulonglong2 *own = reinterpret_cast<const ulonglong2 *>(s.own) + buf * 4 * K::quads + e4;
-                const ulonglong2 *o = reinterpret_cast<const ulonglong2 *>(s.o) + e4;
-                const ulonglong2 sig = own[0], dz = own[K::quads], d = own[2 * K::quads], g = own[3 * K::quads];
-                const ulonglong2 y = o[0], q = o[K::quads], ap = o[2 * K::quads];
+                auto get = [&](const float *plane, int i4) { return reinterpret_cast<const ulonglong2 *>(plane)[i4]; };
+                const int b4 = buf * K::quads + e4;
+                const ulonglong2 sig = get(s.sig, b4), dz = get(s.dz, b4), d = get(s.d, b4), g = get(s.e, b4);
+                const ulonglong2 y = get(s.o, e4), q = get(s.o, K::quads + e4), ap = get(s.o, 2 * K::quads + e4);
                 const f2 sg2[2] = {sig.x, sig.y}, dz2[2] = {dz.x, dz.y}, d2[2] = {d.x, d.y}, g2[2] = {g.x, g.y};
                 const f2 y2[2] = {y.x, y.y}, q2[2] = {q.x, q.y}, ap2[2] = {ap.x, ap.y};
                 f2 x2[2];
@@ -525,15 +535,23 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                 if (gated) store4((T *)a.dz + at, oz, stg.have, sg.vec);
             }
         }
-        for (int e = tid; e < kTile * 2 * K::NP; e += K::threads) {
-            const int j = e / (2 * K::NP), m = e % (2 * K::NP), t = tb + j, st = m % K::NP;
+        for (int e = tid; e < kTile * 2 * LN; e += K::threads) {
+            const int j = e / (2 * LN), q = e / LN % 2, st = e % LN * kNS, t = tb + j;
             if (t < n && st < a.N) {
-                float r = 0.f;
+                f2 r0 = 0, r1 = 0;
 #pragma unroll
-                for (int u = 0; u < K::warps; ++u) r += s.red[(u * kTile + j) * 2 * K::NP + m];
+                for (int u = 0; u < K::warps; ++u) {
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(s.red + u * kTile * 2 * K::NP + e * kNS);
+                    r0 = u ? add2(r0, v.x) : v.x;
+                    r1 = u ? add2(r1, v.y) : v.y;
+                }
                 const long long plane = (long long)a.B * a.T * a.G * a.N;
                 const int ct = (p.c0 - p.g * (a.C / a.G)) / K::width;
-                sg.bc[(2 * (long long)ct + m / K::NP) * plane + (((long long)p.b * a.T + t) * a.G + p.g) * a.N + st] = r;
+                float v[4];
+                unpack2(r0, v[0], v[1]);
+                unpack2(r1, v[2], v[3]);
+                store_states(sg.bc + (2 * (long long)ct + q) * plane + (((long long)p.b * a.T + t) * a.G + p.g) * a.N, st,
+                             a.N, v);
             }
         }
         __syncthreads();
@@ -577,28 +595,36 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
     }
 }
 
-// Joins the parts: the first blocks dC and dB over the channel tiles, the others dA, dD and dbias
-// over batch entries and segments.
+// Joins the parts: the first blocks dC and dB over the channel tiles, 32 elements each with the
+// block's 8 warps over the tiles; the others dA, dD and dbias over batch entries and segments.
 constexpr int kJoin = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoin) scan_bwd_join(ScanArgs a, Seg sg, int tiles, int bc_blocks) {
     if ((int)blockIdx.x < bc_blocks) {
+        __shared__ float red[2][kJoin / 32][32];
         const long long plane = (long long)a.B * a.T * a.G * a.N;
-        const long long e = (long long)blockIdx.x * kJoin + threadIdx.x;
-        if (e >= plane) return;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const long long e = (long long)blockIdx.x * 32 + lane;
         const long long row = e / ((long long)a.G * a.N);
         const int b = (int)(row / a.T), t = (int)(row - (long long)b * a.T);
         float r0 = 0.f, r1 = 0.f;
-        if (t < seq_end(a.lengths, b, a.T)) {
+        if (e < plane && t < seq_end(a.lengths, b, a.T)) {
 #pragma unroll 4
-            for (int i = 0; i < tiles; ++i) {
+            for (int i = warp; i < tiles; i += kJoin / 32) {
                 r0 += sg.bc[2 * i * plane + e];
                 r1 += sg.bc[(2 * i + 1) * plane + e];
             }
         }
-        ((T *)a.dCm)[e] = from_f<T>(r0);
-        ((T *)a.dBm)[e] = from_f<T>(r1);
+        red[0][warp][lane] = r0;
+        red[1][warp][lane] = r1;
+        __syncthreads();
+        if (warp < 2 && e < plane) {
+            float r = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoin / 32; ++w) r += red[warp][w][lane];
+            (warp == 0 ? (T *)a.dCm : (T *)a.dBm)[e] = from_f<T>(r);
+        }
         return;
     }
     const long long e = (long long)(blockIdx.x - bc_blocks) * kJoin + threadIdx.x;
@@ -614,14 +640,14 @@ __global__ void __launch_bounds__(kJoin) scan_bwd_join(ScanArgs a, Seg sg, int t
     *out = r;
 }
 
-int block_threads(int N) { return lanes_for(N) == 1 ? 128 : 256; }
+int block_threads(int N) { return lanes_for(N) == 1 ? 64 : 128; }
 
-// Segments of the backward, from the sizes alone: one where the blocks fill two thirds of the SMs,
-// else enough for two blocks an SM, each of at least 128 tokens.
+// Segments of the backward, from the sizes alone: as many as keep all blocks on the GPU at once (two
+// an SM), each of at least 128 tokens.
 void bwd_segments(int B, int T, int C, int G, int N, int *segs, int *len) {
     const int width = block_threads(N) / lanes_for(N);
     const long long blocks = (long long)B * G * ((C / G + width - 1) / width);
-    long long want = blocks >= 100 ? 1 : (2 * 148 + blocks - 1) / blocks;
+    long long want = 2 * 148 / blocks;
     if (want > T / 128) want = T / 128;
     if (want < 1) want = 1;
     *len = (int)(((T + want - 1) / want + kTile - 1) / kTile * kTile);
@@ -643,7 +669,7 @@ size_t layout(int B, int T, int C, int G, int N, void *ws, Seg *sg) {
     sg->S = take(split ? parts * cn : 0);
     sg->R = take(split ? parts * cn : 0);
     sg->sum = take(split ? parts * C : 0);
-    sg->ckpt = take((size_t)B * ((T + kSub - 1) / kSub) * cn);
+    sg->ckpt = take((size_t)B * ((T + kSub - 1) / kSub) * C * kNS * lanes_for(N));
     sg->bc = take(tiles * 2 * B * T * G * N);
     sg->pA = take(parts * cn);
     sg->pD = take(parts * C);
@@ -668,7 +694,7 @@ la_status bwd_ln(const ScanArgs &a, cudaStream_t st) {
     rc = launch("selective_scan_bwd", scan_bwd_kernel<T, LN>, grid, block, K::smem, st, a, sg, tiles);
     if (rc != LA_OK) return rc;
     const long long plane = (long long)a.B * a.T * a.G * a.N, rest = (long long)a.C * (a.N + 2);
-    const int bc_blocks = (int)((plane + kJoin - 1) / kJoin);
+    const int bc_blocks = (int)((plane + 31) / 32);
     return launch("selective_scan_bwd_join", scan_bwd_join<T>, dim3((unsigned)(bc_blocks + (rest + kJoin - 1) / kJoin)),
                   dim3(kJoin), 0, st, a, sg, tiles, bc_blocks);
 }
