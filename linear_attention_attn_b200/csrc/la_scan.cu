@@ -155,8 +155,8 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
                 const float d1 = pd[(q + j) * K::width];
                 const f2 d = both(d1), u = both(pu[(q + j) * K::width]);
                 const ulonglong2 B = pB[(q + j) * LN];
-                h[0] = fma2(ex2_2(mul2(d, A2[0])), h[0], mul2(u, B.x));
-                h[1] = fma2(ex2_2(mul2(d, A2[1])), h[1], mul2(u, B.y));
+                h[0] = fma2(decay2(d, A2[0]), h[0], mul2(u, B.x));
+                h[1] = fma2(decay2(d, A2[1]), h[1], mul2(u, B.y));
                 if (FULL) {
                     const ulonglong2 C = pC[(q + j) * LN];
                     float y0, y1;

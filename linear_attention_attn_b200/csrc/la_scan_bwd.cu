@@ -286,7 +286,7 @@ scan_bwd_ends(ScanArgs a, Seg sg, int tiles) {
             sum += d1;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const f2 E = ex2_2(mul2(d, A2[k]));
+                const f2 E = decay2(d, A2[k]);
                 h[k] = fma2(E, h[k], mul2(u, B.v[k]));
                 P[k] = mul2(P[k], E);
                 R[k] = fma2(P[k], mul2(e, C.v[k]), R[k]);
@@ -381,7 +381,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (j % kSub == 0) mid[j / kSub][k] = h[k];
-                    h[k] = fma2(ex2_2(mul2(d, A2[k])), h[k], mul2(u, B.v[k]));
+                    h[k] = fma2(decay2(d, A2[k]), h[k], mul2(u, B.v[k]));
                 }
             }
 #pragma unroll
@@ -442,7 +442,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                 const Four B(s.B + bt + j * K::NP);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    E[j][k] = ex2_2(mul2(d, A2[k]));
+                    E[j][k] = decay2(d, A2[k]);
                     H[j][k] = fma2(E[j][k], j ? H[j - 1][k] : hs[k], mul2(u, B.v[k]));
                 }
                 if (gated) {
