@@ -213,45 +213,67 @@ __global__ void __launch_bounds__(512) norm_join(const float2 *part, int parts, 
 
 // --------------------------------------------------------------- tiled groups --
 // A block: one batch entry, one tile of tokens, one chunk of whole groups.  Its threads lie along
-// the chunk's `w` channel vectors, in `rows` rows of tokens; a single group wider than the block
-// is walked in strides (rows = 1).
+// the chunk's `w` vectors of V channels, in `rows` rows of tokens; vectors may lie across group
+// borders (every channel looks up its own group), so V need not divide a group.  A single group
+// wider than the block is walked in strides (rows = 1).
 constexpr int kTiledBlock = 512;
-
-struct Tiling {
-    int gl, gpc, chunks, w, rows, threads, tiles, len;
-};
-
-__device__ __forceinline__ void whereabouts(const Tiling &q, long long block, int &chunk, int &tile, int &b) {
-    chunk = (int)(block % q.chunks);
-    block /= q.chunks;
-    tile = (int)(block % q.tiles);
-    b = (int)(block / q.tiles);
-}
-
 constexpr int kRows = 8;                   // rows that a thread has on their way at a time
 
+struct Tiling {
+    int gpc, chunks, w, rows, threads, tiles, len;
+    __host__ __device__ bool strided() const { return w > threads; }
+};
+
+// What a block of a tiled launch works on.
+struct Where {
+    int chunk, tile, b, cg, g0, ng, w, r, v0, t0, t1;
+    long long base;                        // offset of the chunk's first channel at token 0
+    __device__ __forceinline__ Where(const NormArgs &a, const Tiling &q, int V) {
+        long long block = blockIdx.x;
+        chunk = (int)(block % q.chunks);
+        block /= q.chunks;
+        tile = (int)(block % q.tiles);
+        b = (int)(block / q.tiles);
+        cg = a.C / a.G;
+        g0 = chunk * q.gpc;
+        ng = min(q.gpc, a.G - g0);
+        w = ng * cg / V;
+        r = threadIdx.x / q.w;
+        v0 = threadIdx.x - r * q.w;
+        t0 = tile * q.len;
+        t1 = min(a.T, t0 + q.len);
+        base = (long long)b * a.T * a.C + (long long)g0 * cg;
+    }
+    // tokens of row r of the tile
+    __device__ __forceinline__ int tokens(const Tiling &q, int row) const {
+        return row < q.rows && t0 + row < t1 ? (t1 - t0 - row + q.rows - 1) / q.rows : 0;
+    }
+};
+
+// part [B tiles][G]: a tile's mean and sum of squares about it.
 template <typename T, int V>
-__global__ void __launch_bounds__(kTiledBlock) norm_stats(NormArgs a, Tiling q, float2 *part) {
-    __shared__ float s_n[kTiledBlock], s_mean[kTiledBlock], s_m2[kTiledBlock];
-    int chunk, tile, b;
-    whereabouts(q, blockIdx.x, chunk, tile, b);
-    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
-    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
-    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
-    const T *x = (const T *)a.x + (long long)b * a.T * a.C + (long long)g0 * cg;
+__global__ void __launch_bounds__(kTiledBlock, 2) norm_stats(NormArgs a, Tiling q, float2 *part) {
     typedef Lanes<V> L;
-    float n = 0.f, s = 0.f, m2 = 0.f, pivot = 0.f;
-    if (r < q.rows && t0 + r < t1) {
-        L ls, lq;
+    extern __shared__ float2 s_sum[];      // (mean, M2) of [rows][w V] channels, or of the threads where strided
+    __shared__ int s_n[kTiledBlock];       // strided: values of a thread
+    const Where at(a, q, V);
+    const int rows = at.tokens(q, at.r);
+    const long long step = (long long)q.rows * a.C;
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    if (rows > 0)
+        for (int v = at.v0; v < at.w; v += q.threads) {
+            const T *p = (const T *)a.x + at.base + (long long)(at.t0 + at.r) * a.C + v * V;
+            L pivot, s, sq;
+            {
+                Raw<T, V> first;
+                first.load(p);
+                pivot = first.lanes();
+            }
 #pragma unroll
-        for (int i = 0; i < L::n; ++i) ls.e[i] = lq.e[i] = L::splat(0.f);
-        const long long step = (long long)q.rows * a.C;
-        for (int v = v0; v < w; v += q.threads) {
-            const T *p = x + (long long)(t0 + r) * a.C + v * V;
-            if (n == 0.f) pivot = to_f(*p);
-            const typename L::E minus = L::splat(-pivot);
-            const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
-            n += (float)rows * V;
+            for (int i = 0; i < L::n; ++i) {
+                pivot.e[i] = mul(pivot.e[i], L::splat(-1.f));
+                s.e[i] = sq.e[i] = L::splat(0.f);
+            }
             for (int k = 0; k < rows; k += kRows) {
                 Raw<T, V> row[kRows];
 #pragma unroll
@@ -262,104 +284,129 @@ __global__ void __launch_bounds__(kTiledBlock) norm_stats(NormArgs a, Tiling q, 
                         const L e = row[u].lanes();
 #pragma unroll
                         for (int i = 0; i < L::n; ++i) {
-                            const auto d = add(e.e[i], minus);
-                            ls.e[i] = add(ls.e[i], d);
-                            lq.e[i] = fma(d, d, lq.e[i]);
+                            const auto d = add(e.e[i], pivot.e[i]);
+                            s.e[i] = add(s.e[i], d);
+                            sq.e[i] = fma(d, d, sq.e[i]);
                         }
                     }
                 p += kRows * step;
             }
-        }
-        float vs[V], vq[V];
-        ls.get(vs);
-        lq.get(vq);
+            float vp[V], vs[V], vq[V];
+            pivot.get(vp);
+            s.get(vs);
+            sq.get(vq);
+            const float inv = 1.f / rows;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            s += vs[i];
-            m2 += vq[i];
+            for (int i = 0; i < V; ++i) {
+                const float m = vs[i] * inv, c_mean = m - vp[i], c_m2 = vq[i] - vs[i] * m;
+                if (!q.strided()) {
+                    s_sum[(at.r * q.w + v) * V + i] = make_float2(c_mean, c_m2);
+                } else {
+                    const float d = c_mean - mean, all = n + rows;
+                    mean += d * (rows / all);
+                    m2 += c_m2 + d * d * (n * rows / all);
+                    n = all;
+                }
+            }
         }
+    if (q.strided()) {
+        s_n[threadIdx.x] = (int)n;
+        s_sum[threadIdx.x] = make_float2(mean, m2);
     }
-    s_n[threadIdx.x] = n;
-    s_mean[threadIdx.x] = n > 0.f ? pivot + s / n : 0.f;
-    s_m2[threadIdx.x] = n > 0.f ? m2 - s * (s / n) : 0.f;
     __syncthreads();
-    const int lane = threadIdx.x & 31, members = q.rows * min(q.gl, q.threads);
-    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
-        float cnt = 0.f, sm = 0.f, sq = 0.f;
+    const int lane = threadIdx.x & 31, members = q.strided() ? q.threads : q.rows * at.cg;
+    for (int j = threadIdx.x >> 5; j < at.ng; j += q.threads >> 5) {
+        auto member = [&](int e, float &cnt) {
+            if (q.strided()) {
+                cnt = (float)s_n[e];
+                return s_sum[e];
+            }
+            const int row = e / at.cg;
+            cnt = (float)at.tokens(q, row);
+            return cnt > 0.f ? s_sum[row * q.w * V + j * at.cg + (e - row * at.cg)] : make_float2(0.f, 0.f);
+        };
+        float all = 0.f, sm = 0.f, sq = 0.f, cnt;
         for (int e = lane; e < members; e += 32) {
-            const int er = e / min(q.gl, q.threads), id = er * q.w + j * q.gl + (e - er * min(q.gl, q.threads));
-            cnt += s_n[id];
-            sm = fmaf(s_n[id], s_mean[id], sm);
+            const float2 m = member(e, cnt);
+            all += cnt;
+            sm = fmaf(cnt, m.x, sm);
         }
-        cnt = warp_sum(cnt);
-        const float mean = warp_sum(sm) / cnt;
+        all = warp_sum(all);
+        const float mu = warp_sum(sm) / all;
         for (int e = lane; e < members; e += 32) {
-            const int er = e / min(q.gl, q.threads), id = er * q.w + j * q.gl + (e - er * min(q.gl, q.threads));
-            const float d = s_mean[id] - mean;
-            sq += fmaf(s_n[id] * d, d, s_m2[id]);
+            const float2 m = member(e, cnt);
+            const float d = m.x - mu;
+            sq += fmaf(cnt * d, d, m.y);
         }
         sq = warp_sum(sq);
-        if (lane == 0) part[((long long)b * q.tiles + tile) * a.G + g0 + j] = make_float2(mean, sq);
+        if (lane == 0) part[((long long)at.b * q.tiles + at.tile) * a.G + at.g0 + j] = make_float2(mu, sq);
     }
 }
 
-// gamma (times a factor) and beta of V channels.
+// gamma and beta of V channels from c on.
 template <int V>
-__device__ __forceinline__ void load_affine(const NormArgs &a, int c, float factor, Lanes<V> &ga, Lanes<V> &be) {
+__device__ __forceinline__ void load_affine(const NormArgs &a, int c, Lanes<V> &ga, Lanes<V> &be) {
     float g[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        g[i] = (a.gamma ? a.gamma[c + i] : 1.f) * factor;
+        g[i] = a.gamma ? a.gamma[c + i] : 1.f;
         b[i] = a.beta ? a.beta[c + i] : 0.f;
     }
     ga.set(g);
     be.set(b);
 }
 
+// factor * p[group] of the V channels of vector v, p indexed by the chunk's groups.
+template <int V>
+__device__ __forceinline__ Lanes<V> by_group(const float *p, int v, int cg, float factor) {
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = factor * p[(v * V + i) / cg];
+    Lanes<V> r;
+    r.set(x);
+    return r;
+}
+
 template <typename T, int V>
-__global__ void __launch_bounds__(kTiledBlock) norm_apply(NormArgs a, Tiling q, const float2 *part) {
-    __shared__ float s_mean[kTiledBlock], s_rstd[kTiledBlock];
-    int chunk, tile, b;
-    whereabouts(q, blockIdx.x, chunk, tile, b);
-    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
+__global__ void __launch_bounds__(kTiledBlock, 2) norm_apply(NormArgs a, Tiling q, const float2 *part) {
+    typedef Lanes<V> L;
+    extern __shared__ float s_group[];     // mean, rstd [2][gpc]
+    float *s_mean = s_group, *s_rstd = s_group + q.gpc;
+    const Where at(a, q, V);
     const int lane = threadIdx.x & 31;
-    const float total = (float)a.T * cg;
-    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
-        const float2 *p = part + (long long)b * q.tiles * a.G + g0 + j;
+    const float total = (float)a.T * at.cg;
+    for (int j = threadIdx.x >> 5; j < at.ng; j += q.threads >> 5) {
+        const float2 *p = part + (long long)at.b * q.tiles * a.G + at.g0 + j;
         float sm = 0.f, sq = 0.f;
         for (int i = lane; i < q.tiles; i += 32)
-            sm = fmaf((float)min(q.len, a.T - i * q.len) * cg, p[(long long)i * a.G].x, sm);
+            sm = fmaf((float)min(q.len, a.T - i * q.len) * at.cg, p[(long long)i * a.G].x, sm);
         const float mean = warp_sum(sm) / total;
         for (int i = lane; i < q.tiles; i += 32) {
             const float2 v = p[(long long)i * a.G];
             const float d = v.x - mean;
-            sq += fmaf((float)min(q.len, a.T - i * q.len) * cg * d, d, v.y);
+            sq += fmaf((float)min(q.len, a.T - i * q.len) * at.cg * d, d, v.y);
         }
         const float rstd = 1.f / sqrtf(fmaxf(warp_sum(sq), 0.f) / total + a.eps);
         if (lane == 0) {
             s_mean[j] = mean;
             s_rstd[j] = rstd;
-            if (tile == 0) {
-                if (a.mean) a.mean[(long long)b * a.G + g0 + j] = mean;
-                if (a.rstd) a.rstd[(long long)b * a.G + g0 + j] = rstd;
+            if (at.tile == 0) {
+                if (a.mean) a.mean[(long long)at.b * a.G + at.g0 + j] = mean;
+                if (a.rstd) a.rstd[(long long)at.b * a.G + at.g0 + j] = rstd;
             }
         }
     }
     __syncthreads();
-    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
-    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
-    if (r >= q.rows || t0 + r >= t1) return;
-    const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
-    typedef Lanes<V> L;
-    const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
+    const int rows = at.tokens(q, at.r);
+    if (rows == 0) return;
     const long long step = -(long long)q.rows * a.C;
-    for (int v = v0; v < w; v += q.threads) {
-        const int j = v / q.gl;
-        const float rstd = s_rstd[j];
-        const typename L::E minus = L::splat(-s_mean[j]);
+    for (int v = at.v0; v < at.w; v += q.threads) {
+        const L minus = by_group<V>(s_mean, v, at.cg, -1.f), rstd = by_group<V>(s_rstd, v, at.cg, 1.f);
         L ga, be;
-        load_affine<V>(a, g0 * cg + v * V, rstd, ga, be);
-        long long o = base + v * V + (long long)(t0 + r) * a.C - (rows - 1) * step;      // the last row
+        load_affine<V>(a, at.g0 * at.cg + v * V, ga, be);
+#pragma unroll
+        for (int i = 0; i < L::n; ++i) ga.e[i] = mul(ga.e[i], rstd.e[i]);
+        long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C - (rows - 1) * step;      // the last row
         for (int k = 0; k < rows; k += kRows) {
             // all loads before the first store, which the compiler may not pass (y may be x)
             Raw<T, V> row[kRows];
@@ -369,7 +416,7 @@ __global__ void __launch_bounds__(kTiledBlock) norm_apply(NormArgs a, Tiling q, 
             for (int u = 0; u < kRows; ++u) {
                 L e = row[u].lanes();
 #pragma unroll
-                for (int i = 0; i < L::n; ++i) e.e[i] = act_of(fma(add(e.e[i], minus), ga.e[i], be.e[i]), a.silu);
+                for (int i = 0; i < L::n; ++i) e.e[i] = act_of(fma(add(e.e[i], minus.e[i]), ga.e[i], be.e[i]), a.silu);
                 if (k + u < rows) store_lanes<V>((T *)a.y + o + u * step, e);
             }
             o += kRows * step;
@@ -379,45 +426,38 @@ __global__ void __launch_bounds__(kTiledBlock) norm_apply(NormArgs a, Tiling q, 
 
 // Sums of a tile: chan [B tiles][C] (sum g xh, sum g), part [B tiles][G] (sum gamma g, sum gamma g xh).
 template <typename T, int V>
-__global__ void __launch_bounds__(kTiledBlock) norm_bwd_sums(NormArgs a, Tiling q, float2 *part, float2 *chan) {
-    __shared__ float2 s_g[kTiledBlock];
-    extern __shared__ float2 s_c[];                       // [rows][w V], rows > 1
-    int chunk, tile, b;
-    whereabouts(q, blockIdx.x, chunk, tile, b);
-    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
-    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
-    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
-    const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
-    float2 *out = chan + ((long long)b * q.tiles + tile) * a.C + (long long)g0 * cg;
-    float2 grp = make_float2(0.f, 0.f);
+__global__ void __launch_bounds__(kTiledBlock, 2) norm_bwd_sums(NormArgs a, Tiling q, float2 *part, float2 *chan) {
     typedef Lanes<V> L;
-    if (r < q.rows)
-        for (int v = v0; v < w; v += q.threads) {
-            const int j = v / q.gl;
-            const float mean = a.mean_in[(long long)b * a.G + g0 + j], rstd = a.rstd_in[(long long)b * a.G + g0 + j];
-            const typename L::E minus = L::splat(-mean), scale = L::splat(rstd);
+    extern __shared__ float2 s_sum[];      // channels' sums [rows][w V], or the threads' of the group where strided
+    const Where at(a, q, V);
+    const int rows = at.tokens(q, at.r), width = at.w * V;
+    const long long step = (long long)q.rows * a.C;
+    const float *mean = a.mean_in + (long long)at.b * a.G + at.g0, *rstd = a.rstd_in + (long long)at.b * a.G + at.g0;
+    float2 *out = chan + ((long long)at.b * q.tiles + at.tile) * a.C + (long long)at.g0 * at.cg;
+    float2 grp = make_float2(0.f, 0.f);
+    if (at.r < q.rows)
+        for (int v = at.v0; v < at.w; v += q.threads) {
+            const L minus = by_group<V>(mean, v, at.cg, -1.f), scale = by_group<V>(rstd, v, at.cg, 1.f);
             L ga, be, dg, db;
-            load_affine<V>(a, g0 * cg + v * V, 1.f, ga, be);
+            load_affine<V>(a, at.g0 * at.cg + v * V, ga, be);
 #pragma unroll
             for (int i = 0; i < L::n; ++i) dg.e[i] = db.e[i] = L::splat(0.f);
-            const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
-            const long long step = (long long)q.rows * a.C;
-            const T *x = (const T *)a.x + base + (long long)(t0 + r) * a.C + v * V;
-            const T *dy = (const T *)a.dy + base + (long long)(t0 + r) * a.C + v * V;
+            const T *x = (const T *)a.x + at.base + (long long)(at.t0 + at.r) * a.C + v * V;
+            const T *dy = (const T *)a.dy + at.base + (long long)(at.t0 + at.r) * a.C + v * V;
             constexpr int U = kRows / 2;
             for (int k = 0; k < rows; k += U) {
                 Raw<T, V> rx[U], rg[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     rx[u].load(x + u * step, k + u < rows);
-                    rg[u].load(dy + u * step, k + u < rows);           // 0 behind the tile: adds nothing
+                    rg[u].load(dy + u * step, k + u < rows);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const L e = rx[u].lanes(), d = rg[u].lanes();
 #pragma unroll
                     for (int i = 0; i < L::n; ++i) {
-                        const auto xh = mul(add(e.e[i], minus), scale);
+                        const auto xh = mul(add(e.e[i], minus.e[i]), scale.e[i]);
                         auto g = through_act(d.e[i], fma(xh, ga.e[i], be.e[i]), a.silu);
                         if (k + u >= rows) g = L::splat(0.f);
                         db.e[i] = add(db.e[i], g);
@@ -433,55 +473,61 @@ __global__ void __launch_bounds__(kTiledBlock) norm_bwd_sums(NormArgs a, Tiling 
             db.get(vdb);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                grp.x = fmaf(vga[i], vdb[i], grp.x);
-                grp.y = fmaf(vga[i], vdg[i], grp.y);
-                if (q.rows == 1) out[v * V + i] = make_float2(vdg[i], vdb[i]);
-                else s_c[(r * q.w + v) * V + i] = make_float2(vdg[i], vdb[i]);
+                if (!q.strided()) {
+                    s_sum[(at.r * q.w + v) * V + i] = make_float2(vdg[i], vdb[i]);
+                } else {
+                    out[v * V + i] = make_float2(vdg[i], vdb[i]);
+                    grp.x = fmaf(vga[i], vdb[i], grp.x);
+                    grp.y = fmaf(vga[i], vdg[i], grp.y);
+                }
             }
         }
-    s_g[threadIdx.x] = grp;
+    if (q.strided()) s_sum[threadIdx.x] = grp;
     __syncthreads();
-    if (q.rows > 1)
-        for (int e = threadIdx.x; e < w * V; e += q.threads) {
-            float2 s = s_c[e];
+    if (!q.strided()) {
+        for (int e = threadIdx.x; e < width; e += q.threads) {
+            float2 s = s_sum[e];
             for (int k = 1; k < q.rows; ++k) {
-                const float2 u = s_c[k * q.w * V + e];
+                const float2 u = s_sum[k * q.w * V + e];
                 s.x += u.x;
                 s.y += u.y;
             }
             out[e] = s;
+            const float ga = a.gamma ? a.gamma[at.g0 * at.cg + e] : 1.f;
+            s_sum[e] = make_float2(ga * s.y, ga * s.x);          // what the group sums up
         }
-    const int lane = threadIdx.x & 31, gm = min(q.gl, q.threads), members = q.rows * gm;
-    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
+        __syncthreads();
+    }
+    const int lane = threadIdx.x & 31, members = q.strided() ? q.threads : at.cg;
+    for (int j = threadIdx.x >> 5; j < at.ng; j += q.threads >> 5) {
         float s0 = 0.f, s1 = 0.f;
         for (int e = lane; e < members; e += 32) {
-            const int er = e / gm;
-            const float2 u = s_g[er * q.w + j * q.gl + (e - er * gm)];
+            const float2 u = s_sum[j * at.cg + e];               // strided: a single group, j = 0
             s0 += u.x;
             s1 += u.y;
         }
         s0 = warp_sum(s0);
         s1 = warp_sum(s1);
-        if (lane == 0) part[((long long)b * q.tiles + tile) * a.G + g0 + j] = make_float2(s0, s1);
+        if (lane == 0) part[((long long)at.b * q.tiles + at.tile) * a.G + at.g0 + j] = make_float2(s0, s1);
     }
 }
 
 // dx; the blocks from `main_blocks` on join dgamma and dbeta instead.
 template <typename T, int V>
-__global__ void __launch_bounds__(kTiledBlock)
+__global__ void __launch_bounds__(kTiledBlock, 2)
 norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, unsigned main_blocks) {
-    __shared__ float s_m0[kTiledBlock], s_m1[kTiledBlock];
+    typedef Lanes<V> L;
+    extern __shared__ float s_group[];     // mean(gamma g), mean(gamma g xh) [2][gpc]
+    float *s_m0 = s_group, *s_m1 = s_group + q.gpc;
     if (blockIdx.x >= main_blocks) {
         join_channels(chan, a.B * q.tiles, a.C, blockIdx.x - main_blocks, a.dgamma, a.dbeta);
         return;
     }
-    int chunk, tile, b;
-    whereabouts(q, blockIdx.x, chunk, tile, b);
-    const int cg = a.C / a.G, g0 = chunk * q.gpc, ng = min(q.gpc, a.G - g0), w = ng * q.gl;
+    const Where at(a, q, V);
     const int lane = threadIdx.x & 31;
-    const float inv = 1.f / ((float)a.T * cg);
-    for (int j = threadIdx.x >> 5; j < ng; j += q.threads >> 5) {
-        const float2 *p = part + (long long)b * q.tiles * a.G + g0 + j;
+    const float inv = 1.f / ((float)a.T * at.cg);
+    for (int j = threadIdx.x >> 5; j < at.ng; j += q.threads >> 5) {
+        const float2 *p = part + (long long)at.b * q.tiles * a.G + at.g0 + j;
         float s0 = 0.f, s1 = 0.f;
         for (int i = lane; i < q.tiles; i += 32) {
             const float2 v = p[(long long)i * a.G];
@@ -496,21 +542,16 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
         }
     }
     __syncthreads();
-    const int r = threadIdx.x / q.w, v0 = threadIdx.x - r * q.w;
-    const int t0 = tile * q.len, t1 = min(a.T, t0 + q.len);
-    if (r >= q.rows || t0 + r >= t1) return;
-    const long long base = (long long)b * a.T * a.C + (long long)g0 * cg;
-    typedef Lanes<V> L;
-    const int rows = (t1 - t0 - r + q.rows - 1) / q.rows;
+    const int rows = at.tokens(q, at.r);
+    if (rows == 0) return;
     const long long step = -(long long)q.rows * a.C;
-    for (int v = v0; v < w; v += q.threads) {
-        const int j = v / q.gl;
-        const float mean = a.mean_in[(long long)b * a.G + g0 + j], rstd = a.rstd_in[(long long)b * a.G + g0 + j];
-        const typename L::E minus = L::splat(-mean), scale = L::splat(rstd), m0 = L::splat(-s_m0[j]),
-                            m1 = L::splat(-s_m1[j]);
+    const float *mean = a.mean_in + (long long)at.b * a.G + at.g0, *rstd = a.rstd_in + (long long)at.b * a.G + at.g0;
+    for (int v = at.v0; v < at.w; v += q.threads) {
+        const L minus = by_group<V>(mean, v, at.cg, -1.f), scale = by_group<V>(rstd, v, at.cg, 1.f);
+        const L m0 = by_group<V>(s_m0, v, at.cg, -1.f), m1 = by_group<V>(s_m1, v, at.cg, -1.f);
         L ga, be;
-        load_affine<V>(a, g0 * cg + v * V, 1.f, ga, be);
-        long long o = base + v * V + (long long)(t0 + r) * a.C - (rows - 1) * step;      // the last row
+        load_affine<V>(a, at.g0 * at.cg + v * V, ga, be);
+        long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C - (rows - 1) * step;      // the last row
         constexpr int U = kRows / 2;
         for (int k = 0; k < rows; k += U) {
             // all loads before the first store, which the compiler may not pass (dx may be dy)
@@ -526,9 +567,9 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
                 L d = rg[u].lanes();
 #pragma unroll
                 for (int i = 0; i < L::n; ++i) {
-                    const auto xh = mul(add(e.e[i], minus), scale);
+                    const auto xh = mul(add(e.e[i], minus.e[i]), scale.e[i]);
                     const auto g = through_act(d.e[i], fma(xh, ga.e[i], be.e[i]), a.silu);
-                    d.e[i] = mul(scale, fma(xh, m1, fma(g, ga.e[i], m0)));
+                    d.e[i] = mul(scale.e[i], fma(xh, m1.e[i], fma(g, ga.e[i], m0.e[i])));
                 }
                 if (k + u < rows) store_lanes<V>((T *)a.dx + o + u * step, d);
             }
@@ -553,14 +594,30 @@ int most_tiles(int B, int T) {
     return (int)(n < T ? n : T);
 }
 
+// Groups of a chunk for vectors of V channels: as many as fill a block's threads, in whole vectors
+// (0: none).
+int chunk_groups(const NormArgs &a, int V) {
+    const long long cg = a.C / a.G;
+    if (a.C <= (long long)kTiledBlock * V) return a.G;
+    for (long long g = kTiledBlock * (long long)V / cg; g > 1; --g)
+        if (g * cg % V == 0) return (int)g;
+    return cg % V == 0 ? 1 : 0;
+}
+
+// Widest vector that the addresses allow, divides the rows and leaves whole chunks; at most `most`.
+int tiled_width(const NormArgs &a, int most) {
+    const uintptr_t bits = (uintptr_t)a.x | (uintptr_t)a.y | (uintptr_t)a.dy | (uintptr_t)a.dx;
+    int v = vec_width(elem_bytes(a.dt), a.C, bits);
+    if (v > most) v = most;
+    while (chunk_groups(a, v) == 0) v >>= 1;        // 1 always serves
+    return v;
+}
+
 Tiling tiling(const NormArgs &a, int V) {
     Tiling q;
-    q.gl = a.C / a.G / V;
-    const int fit = q.gl >= kTiledBlock ? 1 : kTiledBlock / q.gl < a.G ? kTiledBlock / q.gl : a.G;
-    q.chunks = (a.G + fit - 1) / fit;
-    q.gpc = (a.G + q.chunks - 1) / q.chunks;
+    q.gpc = chunk_groups(a, V);
     q.chunks = (a.G + q.gpc - 1) / q.gpc;
-    q.w = q.gpc * q.gl;
+    q.w = q.gpc * (a.C / a.G) / V;
     q.rows = q.w >= kTiledBlock ? 1 : kTiledBlock / q.w;
     if (q.rows > a.T) q.rows = a.T;
     const int need = q.rows * q.w;
@@ -573,6 +630,13 @@ Tiling tiling(const NormArgs &a, int V) {
     return q;
 }
 
+// Shared memory of the sums: a pair a channel and row, or a thread.
+size_t sums_smem(const Tiling &q, int V) {
+    const size_t n = q.strided() ? q.threads : (size_t)q.rows * q.w * V;
+    return sizeof(float2) * n;
+}
+
+// The register kernels' vectors lie within a group.
 int width_for(const NormArgs &a) {
     const uintptr_t bits = (uintptr_t)a.x | (uintptr_t)a.y | (uintptr_t)a.dy | (uintptr_t)a.dx;
     return vec_width(elem_bytes(a.dt), (long long)(a.C / a.G), bits);
@@ -598,25 +662,28 @@ void small_lanes(long long nvec, int *L, int *K) {
 }
 
 template <typename T, int V>
-la_status fwd_v(const NormArgs &a, cudaStream_t st) {
-    if (small_fwd(a, V)) {
-        const int nvec = a.T * (a.C / a.G) / V;
-        int L, K;
-        small_lanes(nvec, &L, &K);
-        const long long per = kSmallBlock / L;
-        const dim3 grid((unsigned)(((long long)a.B * a.G + per - 1) / per)), block(kSmallBlock);
-        switch (K) {
-        case 1: return launch("group_norm_fwd", norm_small_fwd<T, V, 1>, grid, block, 0, st, a, L, nvec);
-        case 2: return launch("group_norm_fwd", norm_small_fwd<T, V, 2>, grid, block, 0, st, a, L, nvec);
-        case 4: return launch("group_norm_fwd", norm_small_fwd<T, V, 4>, grid, block, 0, st, a, L, nvec);
-        default: return launch("group_norm_fwd", norm_small_fwd<T, V, 8>, grid, block, 0, st, a, L, nvec);
-        }
+la_status small_fwd_v(const NormArgs &a, cudaStream_t st) {
+    const int nvec = a.T * (a.C / a.G) / V;
+    int L, K;
+    small_lanes(nvec, &L, &K);
+    const long long per = kSmallBlock / L;
+    const dim3 grid((unsigned)(((long long)a.B * a.G + per - 1) / per)), block(kSmallBlock);
+    switch (K) {
+    case 1: return launch("group_norm_fwd", norm_small_fwd<T, V, 1>, grid, block, 0, st, a, L, nvec);
+    case 2: return launch("group_norm_fwd", norm_small_fwd<T, V, 2>, grid, block, 0, st, a, L, nvec);
+    case 4: return launch("group_norm_fwd", norm_small_fwd<T, V, 4>, grid, block, 0, st, a, L, nvec);
+    default: return launch("group_norm_fwd", norm_small_fwd<T, V, 8>, grid, block, 0, st, a, L, nvec);
     }
+}
+
+template <typename T, int V>
+la_status tiled_fwd_v(const NormArgs &a, cudaStream_t st) {
     const Tiling q = tiling(a, V);
     const dim3 grid((unsigned)((long long)a.B * q.tiles * q.chunks)), block(q.threads);
-    la_status rc = launch("group_norm_stats", norm_stats<T, V>, grid, block, 0, st, a, q, (float2 *)a.ws);
+    la_status rc = launch("group_norm_stats", norm_stats<T, V>, grid, block, sums_smem(q, V), st, a, q, (float2 *)a.ws);
     if (rc != LA_OK) return rc;
-    return launch("group_norm_fwd", norm_apply<T, V>, grid, block, 0, st, a, q, (const float2 *)a.ws);
+    return launch("group_norm_fwd", norm_apply<T, V>, grid, block, sizeof(float) * 2 * q.gpc, st, a, q,
+                  (const float2 *)a.ws);
 }
 
 // Batch rows a block of the T = 1 backward walks over: about four blocks an SM, at most 256 parts.
@@ -641,43 +708,71 @@ la_status small_bwd_k(const NormArgs &a, int L, int nvec, int per, float2 *part,
 }
 
 template <typename T, int V>
-la_status bwd_v(const NormArgs &a, cudaStream_t st) {
+la_status small_bwd_v(const NormArgs &a, cudaStream_t st) {
     const bool join = a.dgamma || a.dbeta;
-    if (small_bwd(a.T, a.C / a.G)) {
-        const int nvec = a.C / a.G / V;
-        const int L = nvec > 64 ? kSmallBlock : nvec >= 32 ? 32 : pow2_at_least(nvec);
-        const int per = rows_per_block(a.B, a.G), splits = (a.B + per - 1) / per;
-        float2 *part = join ? (float2 *)a.ws : nullptr;
-        la_status rc;
-        switch (pow2_at_least((nvec + L - 1) / L)) {
-        case 1: rc = small_bwd_k<T, V, 1>(a, L, nvec, per, part, st); break;
-        case 2: rc = small_bwd_k<T, V, 2>(a, L, nvec, per, part, st); break;
-        case 4: rc = small_bwd_k<T, V, 4>(a, L, nvec, per, part, st); break;
-        case 8: rc = small_bwd_k<T, V, 8>(a, L, nvec, per, part, st); break;
-        default: rc = small_bwd_k<T, V, 16>(a, L, nvec, per, part, st); break;
-        }
-        if (rc != LA_OK || !join) return rc;
-        return launch("group_norm_bwd_join", norm_join, dim3((a.C + 31) / 32), dim3(512), 0, st, (const float2 *)part,
-                      splits, a.C, a.dgamma, a.dbeta);
+    const int nvec = a.C / a.G / V;
+    const int L = nvec > 64 ? kSmallBlock : nvec >= 32 ? 32 : pow2_at_least(nvec);
+    const int per = rows_per_block(a.B, a.G), splits = (a.B + per - 1) / per;
+    float2 *part = join ? (float2 *)a.ws : nullptr;
+    la_status rc;
+    switch (pow2_at_least((nvec + L - 1) / L)) {
+    case 1: rc = small_bwd_k<T, V, 1>(a, L, nvec, per, part, st); break;
+    case 2: rc = small_bwd_k<T, V, 2>(a, L, nvec, per, part, st); break;
+    case 4: rc = small_bwd_k<T, V, 4>(a, L, nvec, per, part, st); break;
+    case 8: rc = small_bwd_k<T, V, 8>(a, L, nvec, per, part, st); break;
+    default: rc = small_bwd_k<T, V, 16>(a, L, nvec, per, part, st); break;
     }
+    if (rc != LA_OK || !join) return rc;
+    return launch("group_norm_bwd_join", norm_join, dim3((a.C + 31) / 32), dim3(512), 0, st, (const float2 *)part,
+                  splits, a.C, a.dgamma, a.dbeta);
+}
+
+template <typename T, int V>
+la_status tiled_bwd_v(const NormArgs &a, cudaStream_t st) {
+    const bool join = a.dgamma || a.dbeta;
     const Tiling q = tiling(a, V);
     float2 *part = (float2 *)a.ws, *chan = (float2 *)((char *)a.ws + up256(sizeof(float2) * a.B * q.tiles * a.G));
     const unsigned blocks = (unsigned)((long long)a.B * q.tiles * q.chunks);
-    const size_t smem = q.rows > 1 ? sizeof(float2) * q.rows * q.w * V : 0;
-    la_status rc = launch("group_norm_bwd_sums", norm_bwd_sums<T, V>, dim3(blocks), dim3(q.threads), smem, st, a, q,
-                          part, chan);
+    la_status rc = launch("group_norm_bwd_sums", norm_bwd_sums<T, V>, dim3(blocks), dim3(q.threads), sums_smem(q, V),
+                          st, a, q, part, chan);
     if (rc != LA_OK) return rc;
     return launch("group_norm_bwd", norm_bwd_apply<T, V>, dim3(blocks + (join ? (a.C + 31) / 32 : 0)),
-                  dim3(q.threads), 0, st, a, q, (const float2 *)part, (const float2 *)chan, blocks);
+                  dim3(q.threads), sizeof(float) * 2 * q.gpc, st, a, q, (const float2 *)part, (const float2 *)chan,
+                  blocks);
 }
 
+// The tiled kernels take at most 4 channels a vector: 8 of 16 bits leave no registers for as many rows
+// on their way (B2 T65536 C640 f16 sums: 63 us at 8, 46 us at 4).
 template <typename T>
 la_status norm_t(bool bwd, const NormArgs &a, cudaStream_t st) {
-    switch (width_for(a)) {
-    case 8: return bwd ? bwd_v<T, 16 / sizeof(T)>(a, st) : fwd_v<T, 16 / sizeof(T)>(a, st);
-    case 4: return bwd ? bwd_v<T, 4>(a, st) : fwd_v<T, 4>(a, st);
-    case 2: return bwd ? bwd_v<T, 2>(a, st) : fwd_v<T, 2>(a, st);
-    default: return bwd ? bwd_v<T, 1>(a, st) : fwd_v<T, 1>(a, st);
+    const int v = width_for(a);
+    if (bwd && small_bwd(a.T, a.C / a.G)) {
+        switch (v) {
+        case 8: return small_bwd_v<T, 16 / sizeof(T)>(a, st);
+        case 4: return small_bwd_v<T, 4>(a, st);
+        case 2: return small_bwd_v<T, 2>(a, st);
+        default: return small_bwd_v<T, 1>(a, st);
+        }
+    }
+    if (bwd) {
+        switch (tiled_width(a, 4)) {
+        case 4: return tiled_bwd_v<T, 4>(a, st);
+        case 2: return tiled_bwd_v<T, 2>(a, st);
+        default: return tiled_bwd_v<T, 1>(a, st);
+        }
+    }
+    if (small_fwd(a, v)) {
+        switch (v) {
+        case 8: return small_fwd_v<T, 16 / sizeof(T)>(a, st);
+        case 4: return small_fwd_v<T, 4>(a, st);
+        case 2: return small_fwd_v<T, 2>(a, st);
+        default: return small_fwd_v<T, 1>(a, st);
+        }
+    }
+    switch (tiled_width(a, 4)) {
+    case 4: return tiled_fwd_v<T, 4>(a, st);
+    case 2: return tiled_fwd_v<T, 2>(a, st);
+    default: return tiled_fwd_v<T, 1>(a, st);
     }
 }
 

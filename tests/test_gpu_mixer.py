@@ -366,7 +366,8 @@ NORM = [("f32", 2, 37, 64, 8, "silu"), ("f16", 3, 300, 60, 30, "silu"), ("bf16",
         ("bf16", 300, 1, 512, 8, "silu"), ("f32", 5, 1, 33, 11, "none"), ("f16", 2, 4099, 40, 4, "silu"),
         ("f32", 1, 17, 1290, 1, "silu"), ("bf16", 7, 1, 4096, 1, "silu"), ("f32", 3, 1, 4097, 1, "none"),
         ("f16", 2, 5, 2600, 2, "silu"), ("f32", 1, 2, 3, 3, "silu"), ("bf16", 4, 64, 256, 32, "silu"),
-        ("f16", 40, 1, 9000, 3, "silu"), ("bf16", 3, 3, 30, 15, "none")]
+        ("f16", 40, 1, 9000, 3, "silu"), ("bf16", 3, 3, 30, 15, "none"), ("bf16", 1, 900, 6000, 6, "silu"),
+        ("f16", 2, 500, 4100, 50, "silu"), ("f32", 2, 130, 8200, 1, "silu"), ("f16", 1, 70, 9225, 9, "none")]
 
 
 @pytest.mark.parametrize("dtype,B,T,C,G,act", NORM)
