@@ -219,6 +219,17 @@ __global__ void __launch_bounds__(512) norm_join(const float2 *part, int parts, 
 constexpr int kTiledBlock = 512;
 constexpr int kRows = 8;                   // rows that a thread has on their way at a time
 
+// Calls f(first row, full) for batches of U rows; full says that all rows of the batch exist, so that
+// its loads and stores need no tests.
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+template <int U, typename F>
+__device__ __forceinline__ void batches(int rows, F f) {
+    int k = 0;
+    for (; k + U <= rows; k += U) f(k, Yes());
+    if (k < rows) f(k, No());
+}
+
 struct Tiling {
     int gpc, chunks, w, rows, threads, tiles, len;
     __host__ __device__ bool strided() const { return w > threads; }
@@ -274,13 +285,14 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_stats(NormArgs a, Tiling 
                 pivot.e[i] = mul(pivot.e[i], L::splat(-1.f));
                 s.e[i] = sq.e[i] = L::splat(0.f);
             }
-            for (int k = 0; k < rows; k += kRows) {
+            batches<kRows>(rows, [&](int k, auto full) {
+                constexpr bool FULL = decltype(full)::value;
                 Raw<T, V> row[kRows];
 #pragma unroll
-                for (int u = 0; u < kRows; ++u) row[u].load(p + u * step, k + u < rows);
+                for (int u = 0; u < kRows; ++u) row[u].load(p + u * step, FULL || k + u < rows);
 #pragma unroll
                 for (int u = 0; u < kRows; ++u)
-                    if (k + u < rows) {
+                    if (FULL || k + u < rows) {
                         const L e = row[u].lanes();
 #pragma unroll
                         for (int i = 0; i < L::n; ++i) {
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_stats(NormArgs a, Tiling 
                         }
                     }
                 p += kRows * step;
-            }
+            });
             float vp[V], vs[V], vq[V];
             pivot.get(vp);
             s.get(vs);
@@ -407,20 +419,21 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_apply(NormArgs a, Tiling 
 #pragma unroll
         for (int i = 0; i < L::n; ++i) ga.e[i] = mul(ga.e[i], rstd.e[i]);
         long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C - (rows - 1) * step;      // the last row
-        for (int k = 0; k < rows; k += kRows) {
+        batches<kRows>(rows, [&](int k, auto full) {
+            constexpr bool FULL = decltype(full)::value;
             // all loads before the first store, which the compiler may not pass (y may be x)
             Raw<T, V> row[kRows];
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) row[u].load((const T *)a.x + o + u * step, k + u < rows);
+            for (int u = 0; u < kRows; ++u) row[u].load((const T *)a.x + o + u * step, FULL || k + u < rows);
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 L e = row[u].lanes();
 #pragma unroll
                 for (int i = 0; i < L::n; ++i) e.e[i] = act_of(fma(add(e.e[i], minus.e[i]), ga.e[i], be.e[i]), a.silu);
-                if (k + u < rows) store_lanes<V>((T *)a.y + o + u * step, e);
+                if (FULL || k + u < rows) store_lanes<V>((T *)a.y + o + u * step, e);
             }
             o += kRows * step;
-        }
+        });
     }
 }
 
@@ -445,12 +458,13 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_bwd_sums(NormArgs a, Tili
             const T *x = (const T *)a.x + at.base + (long long)(at.t0 + at.r) * a.C + v * V;
             const T *dy = (const T *)a.dy + at.base + (long long)(at.t0 + at.r) * a.C + v * V;
             constexpr int U = kRows / 2;
-            for (int k = 0; k < rows; k += U) {
+            batches<U>(rows, [&](int k, auto full) {
+                constexpr bool FULL = decltype(full)::value;
                 Raw<T, V> rx[U], rg[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    rx[u].load(x + u * step, k + u < rows);
-                    rg[u].load(dy + u * step, k + u < rows);
+                    rx[u].load(x + u * step, FULL || k + u < rows);
+                    rg[u].load(dy + u * step, FULL || k + u < rows);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -459,14 +473,14 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_bwd_sums(NormArgs a, Tili
                     for (int i = 0; i < L::n; ++i) {
                         const auto xh = mul(add(e.e[i], minus.e[i]), scale.e[i]);
                         auto g = through_act(d.e[i], fma(xh, ga.e[i], be.e[i]), a.silu);
-                        if (k + u >= rows) g = L::splat(0.f);
+                        if (!FULL && k + u >= rows) g = L::splat(0.f);
                         db.e[i] = add(db.e[i], g);
                         dg.e[i] = fma(g, xh, dg.e[i]);
                     }
                 }
                 x += U * step;
                 dy += U * step;
-            }
+            });
             float vga[V], vdg[V], vdb[V];
             ga.get(vga);
             dg.get(vdg);
@@ -553,13 +567,14 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
         load_affine<V>(a, at.g0 * at.cg + v * V, ga, be);
         long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C - (rows - 1) * step;      // the last row
         constexpr int U = kRows / 2;
-        for (int k = 0; k < rows; k += U) {
+        batches<U>(rows, [&](int k, auto full) {
+            constexpr bool FULL = decltype(full)::value;
             // all loads before the first store, which the compiler may not pass (dx may be dy)
             Raw<T, V> rx[U], rg[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                rx[u].load((const T *)a.x + o + u * step, k + u < rows);
-                rg[u].load((const T *)a.dy + o + u * step, k + u < rows);
+                rx[u].load((const T *)a.x + o + u * step, FULL || k + u < rows);
+                rg[u].load((const T *)a.dy + o + u * step, FULL || k + u < rows);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -571,10 +586,10 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
                     const auto g = through_act(d.e[i], fma(xh, ga.e[i], be.e[i]), a.silu);
                     d.e[i] = mul(scale.e[i], fma(xh, m1.e[i], fma(g, ga.e[i], m0.e[i])));
                 }
-                if (k + u < rows) store_lanes<V>((T *)a.dx + o + u * step, d);
+                if (FULL || k + u < rows) store_lanes<V>((T *)a.dx + o + u * step, d);
             }
             o += U * step;
-        }
+        });
     }
 }
 
