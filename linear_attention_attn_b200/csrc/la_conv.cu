@@ -91,9 +91,10 @@ conv_fwd_kernel(ConvArgs a, int cvecs, int segs) {
     constexpr int U = V == 8 ? 4 : 8;          // rows in flight
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (idx >= (long long)a.B * segs * cvecs) return;
-    const long long bs = idx / cvecs;
-    const int c = (int)(idx - bs * cvecs) * V;
-    const int b = (int)(bs / segs), seg = (int)(bs - (long long)b * segs);
+    int c, seg;
+    const long long bs = split(idx, cvecs, c);
+    c *= V;
+    const int b = (int)split(bs, segs, seg);
     const int n = seq_end(a.lengths, b, a.T);
     const int t0 = seg * kSeg, t1 = min(t0 + kSeg, a.T);
     const long long C = a.C;
@@ -369,7 +370,9 @@ __global__ void __launch_bounds__(256) conv_bwd_reduce(const float *part, int pa
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + lane, n = C * (W + 1);
     float s = 0.f;
+    wait_for_stream();
     if (e < n)
+#pragma unroll 8
         for (int p = row; p < parts; p += 8) s += part[(long long)p * n + e];
     red[row][lane] = s;
     __syncthreads();
@@ -417,7 +420,7 @@ la_status bwd_v(const ConvArgs &a, cudaStream_t st) {
     la_status rc = launch("short_conv_bwd", conv_bwd_kernel<T, V, W>, dim3((unsigned)a.B * bt * bc),
                           dim3(32 * kBwdSegs), feed > sums ? feed : sums, st, a, seg, bt, bc, (float *)a.ws);
     if (rc != LA_OK) return rc;
-    return launch("short_conv_bwd_reduce", conv_bwd_reduce, dim3((unsigned)((a.C * (W + 1) + 31) / 32)), dim3(256), 0,
+    return launch_pdl("short_conv_bwd_reduce", conv_bwd_reduce, dim3((unsigned)((a.C * (W + 1) + 31) / 32)), dim3(256), 0,
                   st, (const float *)a.ws, a.B * bt, a.C, W, a.dw, a.dbias);
 }
 

@@ -47,6 +47,24 @@ inline int vec_width(size_t elem, long long unit, uintptr_t address_bits) {
 inline size_t elem_bytes(la_dtype dt) { return dt == LA_F32 ? 4 : 2; }
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// ------------------------------------------------------- index arithmetic --
+// idx / n and the remainder, in 32 bits where idx fits them (a 64-bit division is some 100
+// instructions, more than many of these kernels spend on an element).
+__device__ __forceinline__ long long split(long long idx, int n, int &rest) {
+    if ((idx >> 32) == 0) {
+        const unsigned q = (unsigned)idx / (unsigned)n;
+        rest = (int)((unsigned)idx - q * (unsigned)n);
+        return q;
+    }
+    const long long q = idx / n;
+    rest = (int)(idx - q * n);
+    return q;
+}
+
+// ------------------------------------------------------ dependent launches --
+// A kernel launched by launch_pdl waits here for everything before it in the stream.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // -------------------------------------------------- packed fp32 arithmetic --
 // Two fp32 operations at once on a register pair.  Kernels that work on V neighbouring channels
 // hold them as Lanes<V>: V / 2 pairs, or one float.

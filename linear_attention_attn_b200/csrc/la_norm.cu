@@ -190,6 +190,7 @@ __device__ __forceinline__ void join_channels(const float2 *part, int parts, int
     const int c = block * 32 + lane;
     float2 s = make_float2(0.f, 0.f);
     if (c < C)
+#pragma unroll 8
         for (int p = warp; p < parts; p += warps) {
             const float2 v = part[(long long)p * C + c];
             s.x += v.x;
@@ -208,6 +209,7 @@ __device__ __forceinline__ void join_channels(const float2 *part, int parts, int
 }
 
 __global__ void __launch_bounds__(512) norm_join(const float2 *part, int parts, int C, float *dgamma, float *dbeta) {
+    wait_for_stream();
     join_channels(part, parts, C, blockIdx.x, dgamma, dbeta);
 }
 
@@ -241,10 +243,8 @@ struct Where {
     long long base;                        // offset of the chunk's first channel at token 0
     __device__ __forceinline__ Where(const NormArgs &a, const Tiling &q, int V) {
         long long block = blockIdx.x;
-        chunk = (int)(block % q.chunks);
-        block /= q.chunks;
-        tile = (int)(block % q.tiles);
-        b = (int)(block / q.tiles);
+        block = split(block, q.chunks, chunk);
+        b = (int)split(block, q.tiles, tile);
         cg = a.C / a.G;
         g0 = chunk * q.gpc;
         ng = min(q.gpc, a.G - g0);
@@ -379,24 +379,39 @@ __device__ __forceinline__ Lanes<V> by_group(const float *p, int v, int cg, floa
     return r;
 }
 
+// A lane's part of a group's sums over the tiles, all loads at once (zeros behind the last tile).
+constexpr int kTileTarget = 2 * 148;       // blocks of a tiled launch: two of 512 threads an SM
+constexpr int kTileLoads = (kTileTarget + 31) / 32;
+__device__ __forceinline__ void load_tiles(const float2 *p, int tiles, int G, int lane, float2 (&v)[kTileLoads]) {
+#pragma unroll
+    for (int i = 0; i < kTileLoads; ++i)
+        v[i] = i * 32 + lane < tiles ? p[(long long)(i * 32 + lane) * G] : make_float2(0.f, 0.f);
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kTiledBlock, 2) norm_apply(NormArgs a, Tiling q, const float2 *part) {
     typedef Lanes<V> L;
     extern __shared__ float s_group[];     // mean, rstd [2][gpc]
     float *s_mean = s_group, *s_rstd = s_group + q.gpc;
     const Where at(a, q, V);
+    wait_for_stream();
     const int lane = threadIdx.x & 31;
     const float total = (float)a.T * at.cg;
     for (int j = threadIdx.x >> 5; j < at.ng; j += q.threads >> 5) {
-        const float2 *p = part + (long long)at.b * q.tiles * a.G + at.g0 + j;
+        float2 v[kTileLoads];
+        load_tiles(part + (long long)at.b * q.tiles * a.G + at.g0 + j, q.tiles, a.G, lane, v);
         float sm = 0.f, sq = 0.f;
-        for (int i = lane; i < q.tiles; i += 32)
-            sm = fmaf((float)min(q.len, a.T - i * q.len) * at.cg, p[(long long)i * a.G].x, sm);
+#pragma unroll
+        for (int i = 0; i < kTileLoads; ++i) {
+            const int tile = i * 32 + lane;
+            if (tile < q.tiles) sm = fmaf((float)min(q.len, a.T - tile * q.len) * at.cg, v[i].x, sm);
+        }
         const float mean = warp_sum(sm) / total;
-        for (int i = lane; i < q.tiles; i += 32) {
-            const float2 v = p[(long long)i * a.G];
-            const float d = v.x - mean;
-            sq += fmaf((float)min(q.len, a.T - i * q.len) * at.cg * d, d, v.y);
+#pragma unroll
+        for (int i = 0; i < kTileLoads; ++i) {
+            const int tile = i * 32 + lane;
+            const float d = v[i].x - mean;
+            if (tile < q.tiles) sq += fmaf((float)min(q.len, a.T - tile * q.len) * at.cg * d, d, v[i].y);
         }
         const float rstd = 1.f / sqrtf(fmaxf(warp_sum(sq), 0.f) / total + a.eps);
         if (lane == 0) {
@@ -533,6 +548,7 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
     typedef Lanes<V> L;
     extern __shared__ float s_group[];     // mean(gamma g), mean(gamma g xh) [2][gpc]
     float *s_m0 = s_group, *s_m1 = s_group + q.gpc;
+    wait_for_stream();
     if (blockIdx.x >= main_blocks) {
         join_channels(chan, a.B * q.tiles, a.C, blockIdx.x - main_blocks, a.dgamma, a.dbeta);
         return;
@@ -541,12 +557,13 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
     const int lane = threadIdx.x & 31;
     const float inv = 1.f / ((float)a.T * at.cg);
     for (int j = threadIdx.x >> 5; j < at.ng; j += q.threads >> 5) {
-        const float2 *p = part + (long long)at.b * q.tiles * a.G + at.g0 + j;
+        float2 v[kTileLoads];
+        load_tiles(part + (long long)at.b * q.tiles * a.G + at.g0 + j, q.tiles, a.G, lane, v);
         float s0 = 0.f, s1 = 0.f;
-        for (int i = lane; i < q.tiles; i += 32) {
-            const float2 v = p[(long long)i * a.G];
-            s0 += v.x;
-            s1 += v.y;
+#pragma unroll
+        for (int i = 0; i < kTileLoads; ++i) {
+            s0 += v[i].x;
+            s1 += v[i].y;
         }
         s0 = warp_sum(s0);
         s1 = warp_sum(s1);
@@ -600,8 +617,6 @@ int pow2_at_least(long long n) {
     while (p < n) p *= 2;
     return p;
 }
-
-constexpr int kTileTarget = 2 * 148;       // blocks of a tiled launch: two of 512 threads an SM
 
 // Most tiles of a batch entry, whatever the access width.
 int most_tiles(int B, int T) {
@@ -697,7 +712,7 @@ la_status tiled_fwd_v(const NormArgs &a, cudaStream_t st) {
     const dim3 grid((unsigned)((long long)a.B * q.tiles * q.chunks)), block(q.threads);
     la_status rc = launch("group_norm_stats", norm_stats<T, V>, grid, block, sums_smem(q, V), st, a, q, (float2 *)a.ws);
     if (rc != LA_OK) return rc;
-    return launch("group_norm_fwd", norm_apply<T, V>, grid, block, sizeof(float) * 2 * q.gpc, st, a, q,
+    return launch_pdl("group_norm_fwd", norm_apply<T, V>, grid, block, sizeof(float) * 2 * q.gpc, st, a, q,
                   (const float2 *)a.ws);
 }
 
@@ -738,7 +753,7 @@ la_status small_bwd_v(const NormArgs &a, cudaStream_t st) {
     default: rc = small_bwd_k<T, V, 16>(a, L, nvec, per, part, st); break;
     }
     if (rc != LA_OK || !join) return rc;
-    return launch("group_norm_bwd_join", norm_join, dim3((a.C + 31) / 32), dim3(512), 0, st, (const float2 *)part,
+    return launch_pdl("group_norm_bwd_join", norm_join, dim3((a.C + 31) / 32), dim3(512), 0, st, (const float2 *)part,
                   splits, a.C, a.dgamma, a.dbeta);
 }
 
@@ -751,7 +766,7 @@ la_status tiled_bwd_v(const NormArgs &a, cudaStream_t st) {
     la_status rc = launch("group_norm_bwd_sums", norm_bwd_sums<T, V>, dim3(blocks), dim3(q.threads), sums_smem(q, V),
                           st, a, q, part, chan);
     if (rc != LA_OK) return rc;
-    return launch("group_norm_bwd", norm_bwd_apply<T, V>, dim3(blocks + (join ? (a.C + 31) / 32 : 0)),
+    return launch_pdl("group_norm_bwd", norm_bwd_apply<T, V>, dim3(blocks + (join ? (a.C + 31) / 32 : 0)),
                   dim3(q.threads), sizeof(float) * 2 * q.gpc, st, a, q, (const float2 *)part, (const float2 *)chan,
                   blocks);
 }

@@ -25,9 +25,9 @@ rotary_kernel(RotaryArgs a, int items, int heads_per) {
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long rows = (long long)a.B * a.T;
     if (idx >= rows * items) return;
-    const long long row = idx / items;
-    const int item = (int)(idx - row * items);
-    const int b = (int)(row / a.T), t = (int)(row - (long long)b * a.T);
+    int item, t;
+    const long long row = split(idx, items, item);
+    const int b = (int)split(row, a.T, t);
     const int half = a.R / 2;
     constexpr int W = INTER && V == 1 ? 2 : V;         // elements of an item
     constexpr int P = INTER ? W / 2 : V;               // pairs of an item

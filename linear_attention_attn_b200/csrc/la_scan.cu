@@ -227,10 +227,12 @@ scan_fwd_kernel(ScanArgs a, Seg sg, int tiles) {
         for (int k = 0; k < kNS; ++k) A4[k] *= kLog2e;
     }
     const long long seg0 = ((long long)p.b * sg.segs) * a.C + c, seg_c = (long long)a.C;
+    if (PASS == 2) wait_for_stream();
     if (live) {
         if (PASS == 2) {
             // the state before this segment: segment 0's end, through the segments in between
             load_states(sg.S + seg0 * a.N, n0, a.N, h4);
+#pragma unroll 4
             for (int s = 1; s < p.seg; ++s) {
                 float S[kNS];
                 load_states(sg.S + (seg0 + s * seg_c) * a.N, n0, a.N, S);
@@ -308,13 +310,13 @@ scan_step_kernel(ScanArgs a) {
 }
 
 // Segments of the forward, from the sizes alone: one where the (batch, channel) blocks are at least
-// four an SM; else enough for about eight an SM, each of at least 64 tokens.  Both passes run all
+// four an SM; else enough for about eight an SM, each of at least 32 tokens.  Both passes run all
 // segments but one at once, so fewer than 4 segments gain nothing.
 void fwd_segments(int B, int T, int C, int G, int N, int *segs, int *len) {
     const int width = kThreads / lanes_for(N);
     const long long blocks = (long long)B * G * ((C / G + width - 1) / width);
     long long want = blocks >= 4 * 148 ? 1 : (8 * 148 + blocks - 1) / blocks;
-    if (want > T / 64) want = T / 64;
+    if (want > T / 32) want = T / 32;
     if (want < 4) {
         *segs = 1;
         *len = T;
@@ -342,7 +344,7 @@ la_status fwd_ln(const ScanArgs &a, cudaStream_t st) {
     la_status rc = launch("selective_scan_fwd_ends", scan_fwd_kernel<T, LN, 1>, grid, dim3(kThreads), K::smem, st, a,
                           sg, tiles);
     if (rc != LA_OK) return rc;
-    return launch("selective_scan_fwd", scan_fwd_kernel<T, LN, 2>, grid, dim3(kThreads), K::smem, st, a, sg, tiles);
+    return launch_pdl("selective_scan_fwd", scan_fwd_kernel<T, LN, 2>, grid, dim3(kThreads), K::smem, st, a, sg, tiles);
 }
 
 template <typename T>

@@ -92,12 +92,10 @@ struct Place {
 };
 __device__ __forceinline__ Place place(long long block, int G, int cpg, int tiles, int segs, int width) {
     Place p;
-    const int tile = (int)(block % tiles);
-    block /= tiles;
-    p.g = (int)(block % G);
-    block /= G;
-    p.seg = (int)(block % segs);
-    p.b = (int)(block / segs);
+    int tile;
+    block = split(block, tiles, tile);
+    block = split(block, G, p.g);
+    p.b = (int)split(block, segs, p.seg);
     p.c0 = p.g * cpg + tile * width;
     p.nc = min(width, cpg - tile * width);
     return p;

@@ -318,6 +318,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
     f2 A2[2], h[2], w[2];
+    wait_for_stream();
     {
         float A4[kNS] = {}, h4[kNS] = {}, w4[kNS] = {};
         if (live) {
@@ -329,6 +330,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
             if (a.state_in) load_states(a.state_in + bc, n0, a.N, h4);
             if (a.dstate_in) load_states(a.dstate_in + bc, n0, a.N, w4);
             const long long at = (long long)p.b * sg.segs * a.C + c;
+#pragma unroll 4
             for (int i = 0; i < p.seg; ++i) {
                 const long long q = at + (long long)i * a.C;
                 const float d = sg.sum[q];
@@ -337,6 +339,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
 #pragma unroll
                 for (int k = 0; k < kNS; ++k) h4[k] = fmaf(ex2(d * A4[k]), h4[k], S[k]);
             }
+#pragma unroll 4
             for (int i = sg.segs - 1; i > p.seg; --i) {
                 const long long q = at + (long long)i * a.C;
                 const float d = sg.sum[q];
@@ -601,13 +604,14 @@ constexpr int kJoin = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoin) scan_bwd_join(ScanArgs a, Seg sg, int tiles, int bc_blocks) {
+    wait_for_stream();
     if ((int)blockIdx.x < bc_blocks) {
         __shared__ float red[2][kJoin / 32][32];
         const long long plane = (long long)a.B * a.T * a.G * a.N;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const long long e = (long long)blockIdx.x * 32 + lane;
-        const long long row = e / ((long long)a.G * a.N);
-        const int b = (int)(row / a.T), t = (int)(row - (long long)b * a.T);
+        int t, in_row;
+        const int b = (int)split(split(e, a.G * a.N, in_row), a.T, t);
         float r0 = 0.f, r1 = 0.f;
         if (e < plane && t < seq_end(a.lengths, b, a.T)) {
 #pragma unroll 4
@@ -636,6 +640,7 @@ __global__ void __launch_bounds__(kJoin) scan_bwd_join(ScanArgs a, Seg sg, int t
     if (!out) return;
     const long long step = e < cn ? cn : a.C;
     float r = 0.f;
+#pragma unroll 8
     for (int i = 0; i < a.B * sg.segs; ++i) r += p[i * step];
     *out = r;
 }
@@ -643,12 +648,12 @@ __global__ void __launch_bounds__(kJoin) scan_bwd_join(ScanArgs a, Seg sg, int t
 int block_threads(int N) { return lanes_for(N) == 1 ? 64 : 128; }
 
 // Segments of the backward, from the sizes alone: as many as keep all blocks on the GPU at once (two
-// an SM), each of at least 128 tokens.
+// an SM), each of at least 32 tokens.
 void bwd_segments(int B, int T, int C, int G, int N, int *segs, int *len) {
     const int width = block_threads(N) / lanes_for(N);
     const long long blocks = (long long)B * G * ((C / G + width - 1) / width);
     long long want = 2 * 148 / blocks;
-    if (want > T / 128) want = T / 128;
+    if (want > T / 32) want = T / 32;
     if (want < 1) want = 1;
     *len = (int)(((T + want - 1) / want + kTile - 1) / kTile * kTile);
     *segs = (T + *len - 1) / *len;
@@ -691,11 +696,11 @@ la_status bwd_ln(const ScanArgs &a, cudaStream_t st) {
         rc = launch("selective_scan_bwd_ends", scan_bwd_ends<T, LN>, grid, block, K::smem, st, a, sg, tiles);
         if (rc != LA_OK) return rc;
     }
-    rc = launch("selective_scan_bwd", scan_bwd_kernel<T, LN>, grid, block, K::smem, st, a, sg, tiles);
+    rc = launch_pdl("selective_scan_bwd", scan_bwd_kernel<T, LN>, grid, block, K::smem, st, a, sg, tiles);
     if (rc != LA_OK) return rc;
     const long long plane = (long long)a.B * a.T * a.G * a.N, rest = (long long)a.C * (a.N + 2);
     const int bc_blocks = (int)((plane + 31) / 32);
-    return launch("selective_scan_bwd_join", scan_bwd_join<T>, dim3((unsigned)(bc_blocks + (rest + kJoin - 1) / kJoin)),
+    return launch_pdl("selective_scan_bwd_join", scan_bwd_join<T>, dim3((unsigned)(bc_blocks + (rest + kJoin - 1) / kJoin)),
                   dim3(kJoin), 0, st, a, sg, tiles, bc_blocks);
 }
 
