@@ -16,6 +16,7 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;          // heads whose elements a thread has on their way at a time
 
 // V: elements an access; an interleaved item is at least a pair, of two accesses where V = 1
 // (tensors aligned to one element only).
@@ -48,49 +49,69 @@ rotary_kernel(RotaryArgs a, int items, int heads_per) {
         }
     }
     const int h0 = blockIdx.y * heads_per, h1 = min(h0 + heads_per, a.H + a.Hk);
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-        const bool isq = h < a.H;
-        const long long off =
-            (isq ? ((long long)b * a.H + h) : ((long long)b * a.Hk + (h - a.H))) * a.T * a.D + (long long)t * a.D + c0;
-        const T *src = (const T *)(isq ? a.q : a.k) + off;
-        T *dst = (T *)(isq ? a.oq : a.ok) + off;
-        if (!rot) {
+    const long long stride = (long long)a.T * a.D, at = (long long)t * a.D + c0;
+    constexpr int N = W / V;                           // accesses of an item (of either half)
+    auto heads = [&](const T *src, T *dst, int count) {
+        for (int h = 0; h < count; h += kHeads) {
+            // all loads before the first store, which the compiler may not pass (the output may be the input)
+            Raw<T, V> x[kHeads][N], y[kHeads];
 #pragma unroll
-            for (int j = 0; j < W; j += V)
-                if (c0 + j < a.D) *reinterpret_cast<Pack<T, V> *>(dst + j) = *reinterpret_cast<const Pack<T, V> *>(src + j);
-        } else if constexpr (INTER) {
-            float x[W], y[W];
-            if constexpr (V == 1) {
-                x[0] = to_f(src[0]);
-                x[1] = to_f(src[1]);
-            } else {
-                ldv<V>(src, x);
+            for (int u = 0; u < kHeads; ++u) {
+                const bool there = h + u < count;
+#pragma unroll
+                for (int j = 0; j < N; ++j) x[u][j].load(src + u * stride + j * V, there && (rot || c0 + j * V < a.D));
+                if (!INTER) y[u].load(src + u * stride + half, there && rot);
             }
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                y[2 * i] = fmaf(x[2 * i], cs[i], -x[2 * i + 1] * sn[i]);
-                y[2 * i + 1] = fmaf(x[2 * i], sn[i], x[2 * i + 1] * cs[i]);
-            }
-            if constexpr (V == 1) {
-                dst[0] = from_f<T>(y[0]);
-                dst[1] = from_f<T>(y[1]);
-            } else {
-                stv<V>(dst, y);
-            }
-        } else {
-            float x[V], y[V], u[V], v[V];
-            ldv<V>(src, x);
-            ldv<V>(src + half, y);
+            for (int u = 0; u < kHeads; ++u) {
+                if (h + u >= count) break;
+                T *out = dst + u * stride;
+                if (!rot) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                u[i] = fmaf(x[i], cs[i], -y[i] * sn[i]);
-                v[i] = fmaf(x[i], sn[i], y[i] * cs[i]);
+                    for (int j = 0; j < N; ++j)
+                        if (c0 + j * V < a.D) x[u][j].store(out + j * V);
+                } else if constexpr (INTER) {
+                    float v[W], w[W];
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        float e[V];
+                        x[u][j].lanes().get(e);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[j * V + i] = e[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        w[2 * i] = fmaf(v[2 * i], cs[i], -v[2 * i + 1] * sn[i]);
+                        w[2 * i + 1] = fmaf(v[2 * i], sn[i], v[2 * i + 1] * cs[i]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        float e[V];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) e[i] = w[j * V + i];
+                        stv<V>(out + j * V, e);
+                    }
+                } else {
+                    float v[V], w[V], lo[V], hi[V];
+                    x[u][0].lanes().get(v);
+                    y[u].lanes().get(w);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        lo[i] = fmaf(v[i], cs[i], -w[i] * sn[i]);
+                        hi[i] = fmaf(v[i], sn[i], w[i] * cs[i]);
+                    }
+                    stv<V>(out, lo);
+                    stv<V>(out + half, hi);
+                }
             }
-            stv<V>(dst, u);
-            stv<V>(dst + half, v);
+            src += kHeads * stride;
+            dst += kHeads * stride;
         }
-    }
+    };
+    const int q0 = min(h0, a.H), q1 = min(h1, a.H), k0 = max(h0, a.H) - a.H, k1 = max(h1, a.H) - a.H;
+    const long long qo = ((long long)b * a.H + q0) * stride + at, ko = ((long long)b * a.Hk + k0) * stride + at;
+    heads((const T *)a.q + qo, (T *)a.oq + qo, q1 - q0);
+    heads((const T *)a.k + ko, (T *)a.ok + ko, k1 - k0);
 }
 
 template <typename T, int V, bool INTER>
@@ -100,8 +121,10 @@ la_status rotary_v(const RotaryArgs &a, cudaStream_t st) {
     const long long threads = (long long)a.B * a.T * items;
     const long long blocks = (threads + kThreads - 1) / kThreads;
     const int heads = a.H + a.Hk;
-    // head ranges: about 4 waves of 148 x 8 blocks, at most one range per head
-    long long want = (4 * 148 * 8 + blocks - 1) / blocks;
+    // Head ranges: about one wave of 148 x 8 blocks, at most one range a head.  More ranges pay for the
+    // angles again (4 waves: B8 H32 T1023 D64 f16 18.5 us instead of 12.3, B6 H40 T254 D80 R54 16.4
+    // instead of 10.3; the other way only where they are few: B28 H64 T721 D36 R18 41 instead of 47).
+    long long want = (148 * 8 + blocks - 1) / blocks;
     if (want > heads) want = heads;
     const int per = (int)((heads + want - 1) / want);
     const dim3 grid((unsigned)blocks, (unsigned)((heads + per - 1) / per));
