@@ -27,6 +27,14 @@ la_status refuse(la_status s, const char *fmt, ...) {
 
 bool known(la_dtype dt) { return dt == LA_F32 || dt == LA_F16 || dt == LA_BF16; }
 
+la_status check_ws(size_t need, const void *ws, size_t bytes) {
+    if (need == 0) return LA_OK;
+    if (!ws) return refuse(LA_ERR_WORKSPACE, "workspace is NULL but %zu bytes are needed", need);
+    if ((uintptr_t)ws & 255) return refuse(LA_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
+    if (bytes < need) return refuse(LA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", bytes, need);
+    return LA_OK;
+}
+
 // The tensors of one call: presence, alignment to an element, and that no output overlaps another
 // tensor of the call (in_place: the input that the output may be, exactly).
 class Tensors {
@@ -39,8 +47,12 @@ public:
              const void *in_place = nullptr) {
         add(name, p, count, elem, optional, true, in_place);
     }
-    la_status check() const {
+    // Presence and alignment, then the workspace (`need` bytes, if any), then the overlaps, the
+    // workspace's among them.
+    la_status check(size_t need = 0, const void *ws = nullptr, size_t ws_bytes = 0) {
         if (status_ != LA_OK) return refuse(status_, "%s %s", bad_, status_ == LA_ERR_INVALID_ARG ? "is NULL" : "is not aligned to its element size");
+        LA_TRY(check_ws(need, ws, ws_bytes));
+        if (need) out("workspace", ws, (double)need, 1);
         for (int i = 0; i < n_; ++i) {
             if (!t_[i].out) continue;
             for (int j = 0; j < n_; ++j) {
@@ -122,14 +134,6 @@ size_t need_for(la_op op, int B, int T, int C, int G, int N, la_dtype dt) {
     case LA_OP_GROUP_NORM_BWD: return T == 0 ? 0 : norm_bwd_workspace(B, T, C, G, dt);
     default: return 0;
     }
-}
-
-la_status check_ws(size_t need, const void *ws, size_t bytes) {
-    if (need == 0) return LA_OK;
-    if (!ws) return refuse(LA_ERR_WORKSPACE, "workspace is NULL but %zu bytes are needed", need);
-    if ((uintptr_t)ws & 255) return refuse(LA_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
-    if (bytes < need) return refuse(LA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", bytes, need);
-    return LA_OK;
 }
 
 // A state (or gradient) that passes a call without tokens: `out` becomes `in`, or zeros.
@@ -215,9 +219,7 @@ la_status scan_fwd_entry(bool step, const void *x, const void *dt, const float *
     t.out("y", y, n, es);
     t.out("state_out", state_out, st, 4, !step, state_in);
     const size_t need = step ? 0 : need_for(LA_OP_SELECTIVE_SCAN_FWD, B, T, C, G, N, dtype);
-    if (need && ws) t.out("workspace", ws, (double)need, 1);
-    LA_TRY(t.check());
-    LA_TRY(check_ws(need, ws, ws_bytes));
+    LA_TRY(t.check(need, ws, ws_bytes));
     if (T == 0) return pass_on(state_out, state_in, (size_t)st * 4, (cudaStream_t)stream);
     ScanArgs a = {};
     a.x = x; a.dt_in = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.D = D; a.z = z; a.dt_bias = dt_bias;
@@ -319,9 +321,7 @@ la_status la_short_conv_bwd(const void *x, const float *w, const float *bias, co
     t.out("dw", dw, (double)C * W, 4);
     t.out("dbias", dbias, C, 4, true);
     t.out("dstate_out", dstate_out, st, es, true);
-    if (need && workspace) t.out("workspace", workspace, (double)need, 1);
-    LA_TRY(t.check());
-    LA_TRY(check_ws(need, workspace, workspace_bytes));
+    LA_TRY(t.check(need, workspace, workspace_bytes));
     cudaStream_t s = (cudaStream_t)stream;
     if (T == 0) {
         LA_TRY(pass_on(dw, nullptr, (size_t)C * W * 4, s));
@@ -384,9 +384,7 @@ la_status la_selective_scan_bwd(const void *x, const void *dt, const float *A, c
     t.out("dz", dz, n, es, true);
     t.out("ddt_bias", ddt_bias, C, 4, true);
     t.out("dstate_out", dstate_out, st, 4, true);
-    if (need && workspace) t.out("workspace", workspace, (double)need, 1);
-    LA_TRY(t.check());
-    LA_TRY(check_ws(need, workspace, workspace_bytes));
+    LA_TRY(t.check(need, workspace, workspace_bytes));
     cudaStream_t s = (cudaStream_t)stream;
     if (T == 0) {
         LA_TRY(pass_on(dA, nullptr, (size_t)C * N * 4, s));
@@ -418,9 +416,7 @@ la_status la_group_norm_fwd(const void *x, const float *gamma, const float *beta
     t.out("y", y, n, es, false, x);
     t.out("mean", mean, bg, 4, true);
     t.out("rstd", rstd, bg, 4, true);
-    if (need && workspace) t.out("workspace", workspace, (double)need, 1);
-    LA_TRY(t.check());
-    LA_TRY(check_ws(need, workspace, workspace_bytes));
+    LA_TRY(t.check(need, workspace, workspace_bytes));
     cudaStream_t s = (cudaStream_t)stream;
     if (T == 0) {
         LA_TRY(pass_on(mean, nullptr, (size_t)bg * 4, s));
@@ -449,9 +445,7 @@ la_status la_group_norm_bwd(const void *x, const void *dy, const float *mean, co
     t.out("dx", dx, n, es, false, dy);
     t.out("dgamma", dgamma, C, 4, true);
     t.out("dbeta", dbeta, C, 4, true);
-    if (need && workspace) t.out("workspace", workspace, (double)need, 1);
-    LA_TRY(t.check());
-    LA_TRY(check_ws(need, workspace, workspace_bytes));
+    LA_TRY(t.check(need, workspace, workspace_bytes));
     cudaStream_t s = (cudaStream_t)stream;
     if (T == 0) {
         LA_TRY(pass_on(dgamma, nullptr, (size_t)C * 4, s));
