@@ -77,34 +77,38 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
         Dc[0] = pack2(w[0], w[1]);
         Dc[1] = pack2(w[2], w[3]);
     }
-    Quad<T> rx[K::per], rd[K::per], rz[K::per], rB[K::bper], rC[K::bper];
-    auto load = [&](int tile) {
+    // Two tiles are on their way at a time, in two sets of registers that take turns (a tile's work
+    // alone is about as long as a loaded memory's latency).
+    struct Rows {
+        Quad<T> x[K::per], d[K::per], z[K::per], B[K::bper], C[K::bper];
+    };
+    auto load = [&](int tile, Rows &r) {
         const long long xo = x0 + (long long)tile * kTile * a.C, bo = b0 + (long long)tile * kTile * a.G * a.N;
         const int left = n - t0 - tile * kTile;                       // tokens from the tile's first on
 #pragma unroll
         for (int i = 0; i < K::per; ++i)
             if (K::quads % kThreads == 0 || tid + i * kThreads < K::quads) {
                 const int live = t_first + i * t_step < left ? have : 0;
-                rx[i].load((const T *)a.x + xo + i * xs, live, vec);
-                rd[i].load((const T *)a.dt_in + xo + i * xs, live, vec);
-                if (FULL && a.z) rz[i].load((const T *)a.z + xo + i * xs, live, vec);
+                r.x[i].load((const T *)a.x + xo + i * xs, live, vec);
+                r.d[i].load((const T *)a.dt_in + xo + i * xs, live, vec);
+                if (FULL && a.z) r.z[i].load((const T *)a.z + xo + i * xs, live, vec);
             }
 #pragma unroll
         for (int i = 0; i < K::bper; ++i)
             if (K::bquads % kThreads == 0 || tid + i * kThreads < K::bquads) {
                 const int live = b_first + i * b_step < left ? b_have : 0;
-                rB[i].load((const T *)a.Bm + bo + i * bs, live, bvec);
-                if (FULL) rC[i].load((const T *)a.Cm + bo + i * bs, live, bvec);
+                r.B[i].load((const T *)a.Bm + bo + i * bs, live, bvec);
+                if (FULL) r.C[i].load((const T *)a.Cm + bo + i * bs, live, bvec);
             }
     };
-    auto stage = [&](int tile) {
+    auto stage = [&](int tile, const Rows &r) {
         const int buf = tile & 1, left = n - t0 - tile * kTile;
 #pragma unroll
         for (int i = 0; i < K::per; ++i)
             if (K::quads % kThreads == 0 || tid + i * kThreads < K::quads) {
                 f2 d[2], x[2];
-                rd[i].values(d);
-                rx[i].values(x);
+                r.d[i].values(d);
+                r.x[i].values(x);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     d[j] = add2(d[j], bias[j]);
@@ -120,28 +124,24 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
             if (K::bquads % kThreads == 0 || tid + i * kThreads < K::bquads) {
                 f2 v[2];
                 const int at = buf * K::bquads + tid + i * kThreads;
-                rB[i].values(v);
+                r.B[i].values(v);
                 reinterpret_cast<ulonglong2 *>(s_B)[at] = make_ulonglong2(v[0], v[1]);
                 if (FULL) {
-                    rC[i].values(v);
+                    r.C[i].values(v);
                     reinterpret_cast<ulonglong2 *>(s_C)[at] = make_ulonglong2(v[0], v[1]);
                 }
             }
     };
-    if (tiles > 0) {
-        load(0);
-        stage(0);
-    }
-    __syncthreads();
-    for (int tile = 0; tile < tiles; ++tile) {
+    // `mine` holds this tile's rows and takes those of the one after next, `next` holds the next one's
+    auto work = [&](int tile, Rows &mine, Rows &next) {
         const int buf = tile & 1;
-        Quad<T> kx[K::per], kz[K::per];                       // this tile's, for its outputs
+        Quad<T> kx[K::per], kz[K::per];                       // for this tile's outputs
 #pragma unroll
         for (int i = 0; i < K::per; ++i) {
-            kx[i] = rx[i];
-            kz[i] = rz[i];
+            kx[i] = mine.x[i];
+            kz[i] = mine.z[i];
         }
-        if (tile + 1 < tiles) load(tile + 1);
+        if (tile + 2 < tiles) load(tile + 2, mine);
         const float *pd = s_d + buf * K::pairs + ch, *pu = s_u + buf * K::pairs + ch;
         const ulonglong2 *pB = reinterpret_cast<const ulonglong2 *>(s_B) + buf * K::bquads + nl;
         const ulonglong2 *pC = reinterpret_cast<const ulonglong2 *>(s_C) + buf * K::bquads + nl;
@@ -175,7 +175,7 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
 #pragma unroll
                 for (int j = 0; j < Kept<LN>::value; ++j) sy[(q + j) * K::width] = ys[q / 4][j];
         }
-        if (tile + 1 < tiles) stage(tile + 1);
+        if (tile + 1 < tiles) stage(tile + 1, next);
         __syncthreads();
         if (FULL) {
             const int left = n - t0 - tile * kTile, rows = t1 - t0 - tile * kTile;
@@ -199,6 +199,17 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
                 }
             }
         }
+    };
+    Rows even, odd;
+    if (tiles > 0) {
+        load(0, even);
+        if (tiles > 1) load(1, odd);
+        stage(0, even);
+    }
+    __syncthreads();
+    for (int tile = 0; tile < tiles; tile += 2) {
+        work(tile, even, odd);
+        if (tile + 1 < tiles) work(tile + 1, odd, even);
     }
     if (FULL)
         for (long long e = (long long)tiles * K::pairs + tid; e < (long long)(t1 - t0) * K::width; e += kThreads) {
