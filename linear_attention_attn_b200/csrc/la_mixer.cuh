@@ -22,18 +22,59 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-template <int V, typename T>
-__device__ __forceinline__ void ldv(const T *p, float (&x)[V]) {
-    const Pack<T, V> k = *reinterpret_cast<const Pack<T, V> *>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_f(k.v[i]);
-}
+// Two 16-bit elements as they lie in a word, and back (one rounding each, to nearest even).
+template <typename T> struct Pair16;
+template <> struct Pair16<__half> {
+    static __device__ __forceinline__ float2 widen(unsigned w) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    static __device__ __forceinline__ unsigned narrow(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const unsigned *>(&h);
+    }
+};
+template <> struct Pair16<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 widen(unsigned w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ unsigned narrow(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const unsigned *>(&h);
+    }
+};
+
 template <int V, typename T>
 __device__ __forceinline__ void stv(T *p, const float (&x)[V]) {
-    Pack<T, V> k;
+    if constexpr (sizeof(T) == 2 && V >= 2) {
+        Pack<unsigned, V / 2> k;
 #pragma unroll
-    for (int i = 0; i < V; ++i) k.v[i] = from_f<T>(x[i]);
-    *reinterpret_cast<Pack<T, V> *>(p) = k;
+        for (int i = 0; i < V / 2; ++i) k.v[i] = Pair16<T>::narrow(x[2 * i], x[2 * i + 1]);
+        *reinterpret_cast<Pack<unsigned, V / 2> *>(p) = k;
+    } else {
+        Pack<T, V> k;
+#pragma unroll
+        for (int i = 0; i < V; ++i) k.v[i] = from_f<T>(x[i]);
+        *reinterpret_cast<Pack<T, V> *>(p) = k;
+    }
+}
+// The elements of a word, or of several.
+template <int V, typename T, typename W>
+__device__ __forceinline__ void widen(const W &words, float (&x)[V]) {
+    if constexpr (sizeof(T) == 2 && V >= 2) {
+        Pack<unsigned, V / 2> k;
+        *reinterpret_cast<W *>(&k) = words;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 f = Pair16<T>::widen(k.v[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    } else {
+        Pack<T, V> k;
+        *reinterpret_cast<W *>(&k) = words;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = to_f(k.v[i]);
+    }
 }
 
 // Widest access in elements, a power of two of at most 16 bytes, that divides `unit` (every
@@ -171,11 +212,8 @@ template <typename T, int V> struct Raw {
     }
     __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<typename O::W *>(p) = w; }
     __device__ __forceinline__ Lanes<V> lanes() const {
-        Pack<T, V> k;
-        *reinterpret_cast<typename O::W *>(&k) = w;
         float v[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = to_f(k.v[i]);
+        widen<V, T>(w, v);
         Lanes<V> r;
         r.set(v);
         return r;
@@ -194,6 +232,12 @@ template <int LEFT> __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+template <int V, typename T>
+__device__ __forceinline__ void ldv(const T *p, float (&x)[V]) {
+    Raw<T, V> r;
+    r.load(p);
+    widen<V, T>(r.w, x);
+}
 template <int V, typename T>
 __device__ __forceinline__ void store_lanes(T *p, const Lanes<V> &x) {
     float v[V];

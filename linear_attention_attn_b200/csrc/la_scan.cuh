@@ -144,10 +144,9 @@ template <typename T> struct Quad<T, 2> {
         }
     }
     __device__ __forceinline__ void values(f2 (&v)[2]) const {
-        Pack<T, 4> k;
-        *reinterpret_cast<uint2 *>(&k) = w;
-        v[0] = pack2(to_f(k.v[0]), to_f(k.v[1]));
-        v[1] = pack2(to_f(k.v[2]), to_f(k.v[3]));
+        const float2 a = Pair16<T>::widen(w.x), b = Pair16<T>::widen(w.y);
+        v[0] = pack2(a.x, a.y);
+        v[1] = pack2(b.x, b.y);
     }
 };
 template <typename T> struct Quad<T, 4> {
