@@ -522,7 +522,7 @@ la_status la_short_conv_bwd(const void *x, const float *w, const float *bias, co
  * C a multiple of G; 1 <= N <= 64.  fp32 arithmetic and states.  Workspace:
  * la_mixer_workspace_size(LA_OP_SELECTIVE_SCAN_FWD, ...) (0 unless the sequence is
  * split to fill the GPU).  la_selective_scan_step is T = 1 (no T dimension in the
- * tensors) and always takes and gives the state. */
+ * tensors, B <= 262140) and always takes and gives the state. */
 la_status la_selective_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
                                 const float *D, const void *z, const float *dt_bias, const float *state_in, void *y,
                                 float *state_out, const int *lengths, int softplus, int B, int T, int C, int G, int N,

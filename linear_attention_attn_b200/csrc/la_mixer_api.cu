@@ -203,6 +203,7 @@ la_status scan_fwd_entry(bool step, const void *x, const void *dt, const float *
                          float *state_out, const int *lengths, int softplus, int B, int T, int C, int G, int N,
                          la_dtype dtype, void *ws, size_t ws_bytes, void *stream) {
     LA_TRY(check_scan(B, T, C, G, N, dtype));
+    if (step && B > 262140) return refuse(LA_ERR_UNSUPPORTED, "B must be <= 262140 for a step (got %d)", B);
     const size_t es = elem_bytes(dtype);
     const double n = (double)B * T * C, bc = (double)B * T * G * N, st = (double)B * C * N;
     Tensors t(T == 0);

@@ -276,48 +276,93 @@ scan_fwd_kernel(ScanArgs a, Seg sg, int tiles) {
 
 constexpr int kStepThreads = 128;
 
-// One token: LN lanes a channel; bound by the fp32 state, read and written once.
+// One token of four batch entries for every thread: the lanes of a channel as in the walk, so a warp's
+// states are one run of memory.  All loads are under way before the first is used.  Each of four lanes
+// forms the step of one entry and hands it to the others; the sums over n come back to it the same way.
+// Bound by the fp32 state, read and written once; the rates are read once for the four entries.
 template <typename T, int LN>
 __global__ void __launch_bounds__(kStepThreads)
-scan_step_kernel(ScanArgs a) {
-    const long long idx = (long long)blockIdx.x * kStepThreads + threadIdx.x;
-    const long long bc = idx / LN;
-    const int nl = (int)(idx % LN), n0 = nl * kNS;
-    const bool live = bc < (long long)a.B * a.C;
-    float acc = 0.f, xv = 0.f;
-    int c = 0;
-    if (live) {
-        const int b = (int)(bc / a.C);
-        c = (int)(bc - (long long)b * a.C);
-        const long long bg = ((long long)b * a.G + c / (a.C / a.G)) * a.N;
-        float A[kNS], h[kNS] = {};
-        load_states(a.state_in + bc * a.N, n0, a.N, h);
-        load_states(a.A + (long long)c * a.N, n0, a.N, A);
-        xv = to_f(((const T *)a.x)[bc]);
-        float d = to_f(((const T *)a.dt_in)[bc]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
-        if (a.softplus) d = softplus_f(d);
+scan_step_kernel(ScanArgs a, int vec, int bvec) {
+    constexpr int S = 32 / LN, own = Kept<LN>::value;
+    const int lane = threadIdx.x & 31, nl = lane_states<LN>(), n0 = nl * kNS, r0 = first_token<LN>(nl);
+    const int c = blockIdx.x * (kStepThreads / LN) + lane_channel<LN>(), b0 = blockIdx.y * 4;
+    const bool live = c < a.C;
+    const int rows = live ? min(4, a.B - b0) : 0;
+    const int g = a.G == 1 || !live ? 0 : c / (a.C / a.G);
+    const long long bc = (long long)b0 * a.C + c, bg = ((long long)b0 * a.G + g) * a.N + n0;
+    float4 h[4];
+    Quad<T> Bq[4], Cq[4];
 #pragma unroll
-        for (int k = 0; k < kNS; ++k) {
-            float Bk = 0.f, Ck = 0.f;
-            if (n0 + k < a.N) {
-                Bk = to_f(((const T *)a.Bm)[bg + n0 + k]);
-                Ck = to_f(((const T *)a.Cm)[bg + n0 + k]);
+    for (int r = 0; r < 4; ++r) {
+        const float *p = a.state_in + (bc + (long long)r * a.C) * a.N;
+        h[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            if (vec) {
+                if (n0 < a.N) h[r] = *reinterpret_cast<const float4 *>(p + n0);
+            } else {
+                float v[kNS];
+                load_states(p, n0, a.N, v);
+                h[r] = make_float4(v[0], v[1], v[2], v[3]);
             }
-            h[k] = fmaf(ex2(d * (A[k] * kLog2e)), h[k], d * xv * Bk);
-            acc = fmaf(Ck, h[k], acc);
         }
-        store_states(a.state_out + bc * a.N, n0, a.N, h);
+        const int have = r < rows ? a.N - n0 : 0;
+        Bq[r].load((const T *)a.Bm + bg + (long long)r * a.G * a.N, have, bvec);
+        Cq[r].load((const T *)a.Cm + bg + (long long)r * a.G * a.N, have, bvec);
     }
+    float A[kNS] = {}, d_own[own], u_own[own], x_own[own], z_own[own];
+    if (live) load_states(a.A + (long long)c * a.N, n0, a.N, A);
+    const float bias = live && a.dt_bias ? a.dt_bias[c] : 0.f, D = live && a.D ? a.D[c] : 0.f;
 #pragma unroll
-    for (int m = 1; m < LN; m <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-    if (live && nl == 0) {
-        if (a.D) acc = fmaf(a.D[c], xv, acc);
-        if (a.z) {
-            const float zv = to_f(((const T *)a.z)[bc]);
-            acc *= zv * sigmoid_f(zv);
+    for (int j = 0; j < own; ++j) {
+        const long long at = bc + (long long)(r0 + j) * a.C;
+        float d = 0.f;
+        x_own[j] = z_own[j] = 0.f;
+        if (r0 + j < rows) {
+            x_own[j] = to_f(((const T *)a.x)[at]);
+            d = to_f(((const T *)a.dt_in)[at]) + bias;
+            if (a.z) z_own[j] = to_f(((const T *)a.z)[at]);
         }
-        ((T *)a.y)[bc] = from_f<T>(acc);
+        if (a.softplus) d = softplus_f(d);
+        d_own[j] = d;
+        u_own[j] = d * x_own[j];
     }
+    const f2 A2[2] = {mul2(pack2(A[0], A[1]), both(kLog2e)), mul2(pack2(A[2], A[3]), both(kLog2e))};
+    float sum[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        // the lane that formed this entry's step
+        const int from = (LN == 1 ? 0 : LN == 2 ? r >> 1 : (r >> 1) | (r & 1) << 1) * S + lane % S;
+        const float d = __shfl_sync(0xffffffffu, d_own[r % own], from), u = __shfl_sync(0xffffffffu, u_own[r % own], from);
+        f2 B[2], C[2], s[2] = {pack2(h[r].x, h[r].y), pack2(h[r].z, h[r].w)};
+        Bq[r].values(B);
+        Cq[r].values(C);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) s[k] = fma2(decay2(both(d), A2[k]), s[k], mul2(both(u), B[k]));
+        float y0, y1;
+        unpack2(fma2(C[0], s[0], mul2(C[1], s[1])), y0, y1);
+        sum[r] = y0 + y1;
+        unpack2(s[0], h[r].x, h[r].y);
+        unpack2(s[1], h[r].z, h[r].w);
+        float *p = a.state_out + (bc + (long long)r * a.C) * a.N;
+        if (r < rows) {
+            if (vec) {
+                if (n0 < a.N) *reinterpret_cast<float4 *>(p + n0) = h[r];
+            } else {
+                const float v[kNS] = {h[r].x, h[r].y, h[r].z, h[r].w};
+                store_states(p, n0, a.N, v);
+            }
+        }
+    }
+    reduce4<LN>(sum, nl);
+    if (LN <= 4 || nl < 4)
+#pragma unroll
+        for (int j = 0; j < own; ++j)
+            if (r0 + j < rows) {
+                float y = sum[j];
+                if (a.D) y = fmaf(D, x_own[j], y);
+                if (a.z) y *= z_own[j] * sigmoid_f(z_own[j]);
+                ((T *)a.y)[bc + (long long)(r0 + j) * a.C] = from_f<T>(y);
+            }
 }
 
 // Segments of the forward, from the sizes alone: one where the (batch, channel) blocks are at least
@@ -371,9 +416,10 @@ la_status fwd_t(const ScanArgs &a, cudaStream_t st) {
 
 template <typename T, int LN>
 la_status step_ln(const ScanArgs &a, cudaStream_t st) {
-    const long long n = (long long)a.B * a.C * LN;
-    return launch("selective_scan_step", scan_step_kernel<T, LN>, 
-                  dim3((unsigned)((n + kStepThreads - 1) / kStepThreads)), dim3(kStepThreads), 0, st, a);
+    constexpr int width = kStepThreads / LN;
+    const dim3 grid((unsigned)((a.C + width - 1) / width), (unsigned)((a.B + 3) / 4));
+    return launch("selective_scan_step", scan_step_kernel<T, LN>, grid, dim3(kStepThreads), 0, st, a,
+                  quad_rows<float>(a.N, a.state_in, a.state_out), quad_rows<T>(a.N, a.Bm, a.Cm));
 }
 
 template <typename T>

@@ -52,7 +52,8 @@ __device__ __forceinline__ int seq_end(const int *lengths, int b, int T) {
 // 1.7e-8 to 2.7e-8 on average for results in (1/2, 1) (measured), which a state with a memory of many
 // tokens would gather up; 3e-8 on the argument, in the product's own rounding, brings that average
 // within 1.2e-8 of 0.  A step of 0 still gives exactly 1.
-__device__ __forceinline__ f2 decay2(f2 d, f2 A2) { return ex2_2(fma2(d, A2, both(3e-8f))); }
+constexpr float kNudge = 3e-8f;
+__device__ __forceinline__ f2 decay2(f2 d, f2 A2) { return ex2_2(fma2(d, A2, both(kNudge))); }
 
 // The quarter (of 4 states) that this thread has, and its channel in the block's tile.
 template <int LN> __device__ __forceinline__ int lane_states() { return (threadIdx.x & 31) / (32 / LN); }
