@@ -7,9 +7,9 @@
 // Bound by HBM: every element is read and written once.  A thread owns V elements of one token's
 // row (V of each half in the half layout, V / 2 neighbouring pairs interleaved) and walks over the
 // heads, which share the angle: its sines and cosines stay in registers and are paid for once per
-// head range.  The heads of q and k form one list, cut into as many ranges as give the GPU about
-// four waves of threads, so a single new token spreads over the heads and a long prompt over
-// tokens.
+// head range.  The heads of q and k form one list, cut into as many ranges as fill the GPU, so a
+// single new token spreads over the heads and a long prompt over tokens.
+// B4 H32 + 8 T8192 D128 bf16 (671 MB in and out): 106 us, 6.3 TB/s, 97 % of the measured copy.
 #include "la_mixer.cuh"
 
 namespace la {

@@ -14,10 +14,14 @@
 // kSub tokens in the workspace, then backwards, kSub tokens at a time: their states and decays are
 // formed again in registers (one exponential each) and used in reverse order.  So a state costs two
 // exponentials and about 12 multiply-adds, and 4 / kSub bytes of workspace traffic each way: the
-// kernel is bound by instruction issue, not by HBM.  The sums over channels of dB and dC are
-// butterflies over the lanes of a warp (each step hands half of the values to the partner), then
-// over the block's warps in shared memory, then over the channel tiles in a last launch, always in
-// the same order; that launch also joins the batch entries' parts of dA, dD and dbias.
+// kernel is bound by instructions and their latency, not by HBM.  The sums over channels of dB and dC
+// go through shared memory, first over a warp's lanes, then over the block's warps, then over the
+// channel tiles in a last launch, always in the same order; that launch also joins the batch entries'
+// parts of dA, dD and dbias.
+// Measured at B4 T2048 C2048 N16 bf16: 617 us, where the traffic would take 36 and the exponentials
+// 120; issue slots 39 % busy, shared memory 52 %: 256 blocks of four warps and 254 registers are 1.7
+// warps a scheduler.  More warps by fewer registers or segments cost more than they give (kSub = 4 with
+// 168 registers 747 us, with 128 and two segments 767; two channels a lane 980).
 //
 // Few channels and a long sequence: segments as in the forward.  A first launch gives every
 // segment's end state from zero, S, its sum of d, and the gradient that it hands to the state
