@@ -138,22 +138,38 @@ __global__ void __launch_bounds__(kSmallBlock) norm_small_bwd(NormArgs a, int L,
             dga[k][i] = dbe[k][i] = 0.f;
         }
     const float inv = 1.f / ((float)nvec * V);
-    for (int b = b0; b < b1; ++b) {
+    // the next row's values come while this one's are worked on
+    Raw<T, V> rx[K], rg[K];
+    float mean = 0.f, rstd = 0.f;
+    auto load = [&](int b) {
         const long long base = (long long)b * a.C + (long long)g * cg;
-        const float mean = live ? a.mean_in[(long long)b * a.G + g] : 0.f;
-        const float rstd = live ? a.rstd_in[(long long)b * a.G + g] : 0.f;
-        float xh[K][V], gr[K][V], s[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int e = lane + k * L;
+            rx[k].load((const T *)a.x + base + e * V, live && b < b1 && e < nvec);
+            rg[k].load((const T *)a.dy + base + e * V, live && b < b1 && e < nvec);
+        }
+        mean = live && b < b1 ? a.mean_in[(long long)b * a.G + g] : 0.f;
+        rstd = live && b < b1 ? a.rstd_in[(long long)b * a.G + g] : 0.f;
+    };
+    load(b0);
+    for (int b = b0; b < b1; ++b) {
+        const long long base = (long long)b * a.C + (long long)g * cg;
+        const float mu = mean, rs = rstd;
+        float xh[K][V], gr[K][V], s[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < V; ++i) xh[k][i] = gr[k][i] = 0.f;
+        for (int k = 0; k < K; ++k) {
+            rx[k].lanes().get(xh[k]);
+            rg[k].lanes().get(gr[k]);
+        }
+        load(b + 1);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int e = lane + k * L;
             if (live && e < nvec) {
-                ldv<V>((const T *)a.x + base + e * V, xh[k]);
-                ldv<V>((const T *)a.dy + base + e * V, gr[k]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    xh[k][i] = (xh[k][i] - mean) * rstd;
+                    xh[k][i] = (xh[k][i] - mu) * rs;
                     gr[k][i] = through_act(gr[k][i], fmaf(xh[k][i], ga[k][i], be[k][i]), a.silu);
                     dbe[k][i] += gr[k][i];
                     dga[k][i] = fmaf(gr[k][i], xh[k][i], dga[k][i]);
@@ -170,7 +186,7 @@ __global__ void __launch_bounds__(kSmallBlock) norm_small_bwd(NormArgs a, int L,
             if (live && e < nvec) {
                 float o[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = rstd * (gr[k][i] - s[0] * inv - xh[k][i] * (s[1] * inv));
+                for (int i = 0; i < V; ++i) o[i] = rs * (gr[k][i] - s[0] * inv - xh[k][i] * (s[1] * inv));
                 stv<V>((T *)a.dx + base + e * V, o);
             }
         }
@@ -656,7 +672,9 @@ Tiling tiling(const NormArgs &a, int V) {
     if (q.rows > a.T) q.rows = a.T;
     const int need = q.rows * q.w;
     q.threads = need >= kTiledBlock ? kTiledBlock : (need + 31) / 32 * 32;
-    long long want = (kTileTarget + (long long)a.B * q.chunks - 1) / ((long long)a.B * q.chunks);
+    // rounded down: a few blocks more than fit at once would take a second turn of the whole GPU
+    long long want = kTileTarget / ((long long)a.B * q.chunks);
+    if (want < 1) want = 1;
     const long long most = (a.T + 4 * q.rows - 1) / (4 * q.rows);          // at least 4 tokens a thread
     if (want > most) want = most;
     q.len = (int)((a.T + want - 1) / want);
@@ -720,10 +738,15 @@ la_status tiled_fwd_v(const NormArgs &a, cudaStream_t st) {
                   (const float2 *)a.ws);
 }
 
-// Batch rows a block of the T = 1 backward walks over: about four blocks an SM, at most 256 parts.
-int rows_per_block(int B, int G) {
-    long long splits = 4 * 148LL / ((G + 7) / 8) + 1;
-    if (splits > 256) splits = 256;
+// Lanes of a group in the T = 1 backward.
+int bwd_lanes(int nvec) { return nvec > 64 ? kSmallBlock : nvec >= 32 ? 32 : pow2_at_least(nvec); }
+
+// Batch rows a block of the T = 1 backward walks over: about eight blocks an SM, at most 512 parts (as
+// for aligned tensors: the workspace's size does not go by addresses).
+int rows_per_block(int B, int G, int cg, la_dtype dt) {
+    const int per = kSmallBlock / bwd_lanes(cg / vec_width(elem_bytes(dt), cg, 0));
+    long long splits = 8 * 148LL / ((G + per - 1) / per) + 1;
+    if (splits > 512) splits = 512;
     if (splits > B) splits = B;
     return (int)((B + splits - 1) / splits);
 }
@@ -745,8 +768,8 @@ template <typename T, int V>
 la_status small_bwd_v(const NormArgs &a, cudaStream_t st) {
     const bool join = a.dgamma || a.dbeta;
     const int nvec = a.C / a.G / V;
-    const int L = nvec > 64 ? kSmallBlock : nvec >= 32 ? 32 : pow2_at_least(nvec);
-    const int per = rows_per_block(a.B, a.G), splits = (a.B + per - 1) / per;
+    const int L = bwd_lanes(nvec);
+    const int per = rows_per_block(a.B, a.G, a.C / a.G, a.dt), splits = (a.B + per - 1) / per;
     float2 *part = join ? (float2 *)a.ws : nullptr;
     la_status rc;
     switch (pow2_at_least((nvec + L - 1) / L)) {
@@ -825,10 +848,12 @@ size_t norm_fwd_workspace(int B, int T, int C, int G, la_dtype) {
     return up256(sizeof(float2) * B * most_tiles(B, T) * G);
 }
 
-size_t norm_bwd_workspace(int B, int T, int C, int G, la_dtype) {
+size_t norm_bwd_workspace(int B, int T, int C, int G, la_dtype dt) {
     if (T == 0) return 0;
-    const int per = rows_per_block(B, G), splits = (B + per - 1) / per;
-    if (small_bwd(T, C / G)) return up256(sizeof(float2) * splits * C);
+    if (small_bwd(T, C / G)) {
+        const int per = rows_per_block(B, G, C / G, dt), splits = (B + per - 1) / per;
+        return up256(sizeof(float2) * splits * C);
+    }
     return up256(sizeof(float2) * B * most_tiles(B, T) * G) + up256(sizeof(float2) * B * most_tiles(B, T) * C);
 }
 
