@@ -421,7 +421,8 @@ la_status la_chunk_decay_step(const void *q, const void *k, const void *v, void 
  * Conventions that differ from the attention ops: tensors may start at any
  * address that is a multiple of their element size (16-byte aligned ones with
  * widths in multiples of 16 bytes get the widest accesses); tensor sizes are
- * not limited to 2^31 elements; parameters (weights, rates, biases, scales) and
+ * not limited to 2^31 elements (C <= 2^20, T <= 2^30, B*C < 2^31, B*T*C < 2^40;
+ * rotary: B*T*D < 2^37, H + Hk <= 65535); parameters (weights, rates, biases, scales) and
  * their gradients are fp32.  No output may overlap an input or another output
  * unless its comment allows it.  In a padded batch `lengths` (int32 [B], device,
  * or NULL) gives each sequence's length, taken as 0 or T where it lies outside
