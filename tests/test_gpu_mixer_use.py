@@ -450,3 +450,48 @@ def test_offsets_past_two_to_the_31():
     xh = (end[0].double().view(-1, 32, 128) - mu[:, None]) * rs[:, None]
     wd = (rs[:, None] * (end[0].double().view(-1, 32, 128) - mu[:, None] - xh * m1[:, None])).view(1, tail, C)
     close(y[:, cut:], wd, "norm dx", 800, want.abs().max())
+
+
+def _odd(t):
+    """The same values at an address that only one element divides."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    flat[1:].copy_(t.reshape(-1))
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_addresses_of_one_element_give_the_same_bits(dtype):
+    """Narrow accesses change no sum's order in the convolution and the scan."""
+    blk = StateSpaceBlock(64, 16, 4, 4)
+    ins = blk.inputs(2, 90, dtype)
+    x, dt, Bm, Cm, z = ins
+    ox, odt, oB, oC, oz = (_odd(t) for t in ins)
+    do = _normal(50)(2, 90, 64, dtype=dtype)
+    y, y2 = torch.empty_like(x), _odd(torch.empty_like(x))
+    la.la_short_conv_fwd(x, blk.w, y, bias=blk.bias)
+    la.la_short_conv_fwd(ox, _odd(blk.w), y2, bias=_odd(blk.bias))
+    assert torch.equal(y, y2)
+    dw, dw2 = torch.empty_like(blk.w), torch.empty_like(blk.w)
+    la.la_short_conv_bwd(x, blk.w, do, y, dw)
+    la.la_short_conv_bwd(ox, blk.w, _odd(do), y2, dw2)
+    assert torch.equal(y, y2) and torch.equal(dw, dw2)
+    st, st2 = torch.empty(2, 64, 16, device=_dev()), _odd(torch.empty(2, 64, 16, device=_dev()))
+    la.la_selective_scan_fwd(x, dt, blk.A, Bm, Cm, y, z=z, dt_bias=blk.dt_bias, state_out=st)
+    la.la_selective_scan_fwd(ox, odt, _odd(blk.A), oB, oC, y2, z=oz, dt_bias=blk.dt_bias, state_out=st2)
+    assert torch.equal(y, y2) and torch.equal(st, st2)
+    g, g2 = ([torch.empty_like(t) for t in (x, dt, blk.A, Bm, Cm, z, st)] for _ in range(2))
+    g2 = [_odd(t) for t in g2]
+    la.la_selective_scan_bwd(x, dt, blk.A, Bm, Cm, do, g[0], g[1], g[2], g[3], g[4], z=z, dz=g[5], dt_bias=blk.dt_bias,
+                             state_in=st, dstate_out=g[6])
+    la.la_selective_scan_bwd(ox, odt, _odd(blk.A), oB, oC, _odd(do), g2[0], g2[1], g2[2], g2[3], g2[4], z=oz, dz=g2[5],
+                             dt_bias=blk.dt_bias, state_in=st2, dstate_out=g2[6])
+    for a, b in zip(g, g2):
+        assert torch.equal(a, b)
+    # one token
+    tok = [t[:, 0].contiguous() for t in ins]
+    o, o2 = torch.empty_like(tok[0]), _odd(torch.empty_like(tok[0]))
+    s, s2 = st.clone(), _odd(st)
+    la.la_selective_scan_step(tok[0], tok[1], blk.A, tok[2], tok[3], o, s, z=tok[4])
+    t2 = [_odd(t) for t in tok]
+    la.la_selective_scan_step(t2[0], t2[1], _odd(blk.A), t2[2], t2[3], o2, s2, z=t2[4])
+    assert torch.equal(o, o2) and torch.equal(s, s2)
