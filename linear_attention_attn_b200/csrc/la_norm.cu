@@ -11,7 +11,8 @@
 // walking every tile backwards so that it begins with what the first left in L2 last.
 // Means and squares never meet as large sums: a thread sums about its own first value, and threads
 // and tiles are joined through their means, sum M2_i + n_i (mean_i - mean)^2, so a mean far above
-// the spread costs no precision.  Every sum runs in a fixed order.
+// the spread costs no precision.  Every sum runs in a fixed order.  An infinity (which is no pivot) makes
+// its group's mean infinite, and like a NaN the variance and the whole group NaN, as the formula does.
 // B2 T65536 C640 G32 f16 with SiLU (168 MB in, 168 out): 109 us, where two reads and a write at the
 // measured copy bandwidth would take 77; the second launch's special-function units are 62 % busy
 // (an exponential and a reciprocal an element), the memory 50 %.  B3 T4087 C330 G30 fp32 gradient:
@@ -26,6 +27,8 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
     return v;
 }
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 __device__ __forceinline__ float splat_like(float, float x) { return x; }
 __device__ __forceinline__ f2 splat_like(f2, float x) { return both(x); }
@@ -294,17 +297,16 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_stats(NormArgs a, Tiling 
     if (rows > 0)
         for (int v = at.v0; v < at.w; v += q.threads) {
             const T *p = (const T *)a.x + at.base + (long long)(at.t0 + at.r) * a.C + v * V;
-            L pivot, s, sq;
+            L pivot, s, sq;                // pivot: negated
             {
-                Raw<T, V> first;
-                first.load(p);
-                pivot = first.lanes();
+                float first[V];
+                ldv<V>(p, first);
+#pragma unroll
+                for (int i = 0; i < V; ++i) first[i] = finite(first[i]) ? -first[i] : 0.f;
+                pivot.set(first);
             }
 #pragma unroll
-            for (int i = 0; i < L::n; ++i) {
-                pivot.e[i] = mul(pivot.e[i], L::splat(-1.f));
-                s.e[i] = sq.e[i] = L::splat(0.f);
-            }
+            for (int i = 0; i < L::n; ++i) s.e[i] = sq.e[i] = L::splat(0.f);
             batches<kRows>(rows, [&](int k, auto full) {
                 constexpr bool FULL = decltype(full)::value;
                 Raw<T, V> row[kRows];
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_stats(NormArgs a, Tiling 
                     s_sum[(at.r * q.w + v) * V + i] = make_float2(c_mean, c_m2);
                 } else {
                     const float d = c_mean - mean, all = n + rows;
-                    mean += d * (rows / all);
+                    mean += finite(d) ? d * (rows / all) : c_mean;
                     m2 += c_m2 + d * d * (n * rows / all);
                     n = all;
                 }
@@ -433,7 +435,8 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_apply(NormArgs a, Tiling 
             const float d = v[i].x - mean;
             if (tile < q.tiles) sq += fmaf((float)min(q.len, a.T - tile * q.len) * at.cg * d, d, v[i].y);
         }
-        const float rstd = 1.f / sqrtf(fmaxf(warp_sum(sq), 0.f) / total + a.eps);
+        sq = warp_sum(sq);
+        const float rstd = 1.f / sqrtf((sq < 0.f ? 0.f : sq) / total + a.eps);      // a NaN stays one
         if (lane == 0) {
             s_mean[j] = mean;
             s_rstd[j] = rstd;

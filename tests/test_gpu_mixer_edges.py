@@ -1,0 +1,51 @@
+"""Non-finite values, outlying rows, far positions and narrow accesses of the operators around the
+token mixers, against their 64-bit definitions."""
+import pytest
+import torch
+
+import linear_attention_attn_b200 as la
+from tests import mixer_ref as ref
+from tests.mixer_ref import DTYPES, close
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+
+def _dev():
+    return torch.device("cuda", 0)
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, dtype=torch.float32, scale=1.0):
+        return (torch.randn(shape, generator=g, device=_dev()) * scale).to(dtype)
+    return normal
+
+
+def _same_where_not_finite(got, want, name):
+    """NaN and infinities exactly where the definition has them; returns the mask of the finite rest."""
+    for kind, a, b in (("nan", torch.isnan(got), torch.isnan(want)), ("+inf", got == INF, want == INF),
+                       ("-inf", got == -INF, want == -INF)):
+        assert torch.equal(a, b), "%s: %d %s, %d expected" % (name, int(a.sum()), kind, int(b.sum()))
+    return torch.isfinite(want)
+
+
+# ----------------------------------------------------------------------------------- group norm --
+
+# groups in registers, in tiles, in tiles of an odd width, wider than a block
+@pytest.mark.parametrize("dtype,T,C,G", [("f32", 40, 16, 4), ("f32", 3000, 64, 8), ("bf16", 3000, 64, 8),
+                                         ("f16", 4099, 33, 3), ("f32", 700, 8200, 1)])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("where", [0.0, 0.4, 1.0])
+def test_group_norm_hands_non_finite_values_on(dtype, T, C, G, bad, where):
+    """A NaN or an infinity anywhere in a group: mean as the sum has it, a NaN variance, NaN everywhere."""
+    x = _gen(1)(2, T, C, dtype=DTYPES[dtype])
+    x[1, int(where * (T - 1)), C // G // 2] = bad
+    y, mean, rstd = torch.empty_like(x), torch.empty(2, G, device=_dev()), torch.empty(2, G, device=_dev())
+    la.la_group_norm_fwd(x, y, G, mean=mean, rstd=rstd)
+    wy, wm, wr = ref.norm(x.double(), None, None, G, 1e-5, "none")
+    assert int(torch.isnan(wr).sum()) == 1 and int(torch.isnan(wy).sum()) == T * (C // G)
+    for name, got, want in (("mean", mean, wm), ("rstd", rstd, wr), ("y", y, wy)):
+        ok = _same_where_not_finite(got, want, name)
+        close(got[ok], want[ok], name, 400, 8.0)
