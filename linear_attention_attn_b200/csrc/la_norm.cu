@@ -9,10 +9,11 @@
 // warp, a warp, or a block a group; mean first, then the squares about it).  A larger one takes two
 // launches over the same tiles of tokens, whole rows at a time: sums, then the result, the second
 // walking every tile backwards so that it begins with what the first left in L2 last.
-// Means and squares never meet as large sums: a thread sums about its own first value, and threads
-// and tiles are joined through their means, sum M2_i + n_i (mean_i - mean)^2, so a mean far above
-// the spread costs no precision.  Every sum runs in a fixed order.  An infinity (which is no pivot) makes
-// its group's mean infinite, and like a NaN the variance and the whole group NaN, as the formula does.
+// Means and squares never meet as large sums: a thread sums about its own first value, then about the
+// mean of its first 8, 16, 32, ... values (the first may lie far from the rest), and threads and tiles are
+// joined through their means, sum M2_i + n_i (mean_i - mean)^2, so a mean far above the spread costs no
+// precision.  Every sum runs in a fixed order.  An infinity (which is no pivot) makes its group's mean
+// infinite, and like a NaN the variance and the whole group NaN, as the formula does.
 // B2 T65536 C640 G32 f16 with SiLU (168 MB in, 168 out): 109 us, where two reads and a write at the
 // measured copy bandwidth would take 77; the second launch's special-function units are 62 % busy
 // (an exponential and a reciprocal an element), the memory 50 %.  B3 T4087 C330 G30 fp32 gradient:
@@ -284,6 +285,29 @@ struct Where {
     }
 };
 
+// Moves the (negated) pivot of n values per channel, whose distances from it sum up to s and whose
+// squares to sq, by their mean distance d: s - n d and sq - d (s + (s - n d)).
+template <int V>
+__device__ __forceinline__ void recentre(Lanes<V> &pivot, Lanes<V> &s, Lanes<V> &sq, float n) {
+    float vp[V], vs[V], vq[V];
+    pivot.get(vp);
+    s.get(vs);
+    sq.get(vq);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float to = vp[i] - vs[i] / n, d = vp[i] - to;        // the step as it was rounded
+        if (finite(d)) {
+            const float left = fmaf(-n, d, vs[i]);
+            vq[i] = fmaf(-d, vs[i] + left, vq[i]);
+            vs[i] = left;
+            vp[i] = to;
+        }
+    }
+    pivot.set(vp);
+    s.set(vs);
+    sq.set(vq);
+}
+
 // part [B tiles][G]: a tile's mean and sum of squares about it.
 template <typename T, int V>
 __global__ void __launch_bounds__(kTiledBlock, 2) norm_stats(NormArgs a, Tiling q, float2 *part) {
@@ -324,6 +348,10 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_stats(NormArgs a, Tiling 
                         }
                     }
                 p += kRows * step;
+                // The pivot moves to the mean of the rows so far when their number doubles (8, 16, 32, ...):
+                // about it, sq is at most twice the squares about the mean, however far away the first row lay.
+                const int done = k + kRows;
+                if (FULL && done < rows && (done & (done - 1)) == 0) recentre<V>(pivot, s, sq, (float)done);
             });
             float vp[V], vs[V], vq[V];
             pivot.get(vp);

@@ -49,3 +49,20 @@ def test_group_norm_hands_non_finite_values_on(dtype, T, C, G, bad, where):
     for name, got, want in (("mean", mean, wm), ("rstd", rstd, wr), ("y", y, wy)):
         ok = _same_where_not_finite(got, want, name)
         close(got[ok], want[ok], name, 400, 8.0)
+
+
+@pytest.mark.parametrize("C,G", [(257, 1), (511, 7)])
+def test_group_norm_variance_behind_an_outlying_first_row(C, G):
+    """First rows 10^4 spreads away from thousands of rows that one thread sums up: squares about them
+    would leave the spread to rounding."""
+    B, T = 296, 8192
+    x = _gen(2)(B, T, C)
+    x[:, 0] += 1e4
+    y, mean, rstd = torch.empty_like(x), torch.empty(B, G, device=_dev()), torch.empty(B, G, device=_dev())
+    la.la_group_norm_fwd(x, y, G, mean=mean, rstd=rstd)
+    for b in (0, 17, B - 1):
+        _, wm, wr = ref.norm(x[b:b + 1].double(), None, None, G, 1e-5, "none")
+        # the bounds of the parity tests: 100 and 200 roundings
+        xm = x[b].abs().max().double()
+        close(mean[b:b + 1], wm, "mean", 100, xm)
+        close(rstd[b:b + 1], wr, "rstd", 200, wr * (1 + wr * xm))
