@@ -437,7 +437,8 @@ la_status la_chunk_decay_step(const void *q, const void *k, const void *v, void 
  *      a' = m (a cos(p f_i) - b sin(p f_i)),   b' = m (a sin(p f_i) + b cos(p f_i));
  * entries from R on are copied.  The backward turns by -p f_i (with the same
  * magnitude): the gradient of the forward.  The angle is formed and reduced in
- * 64 bits, so far positions lose nothing.
+ * twice 64 bits, so far positions, up to 2^53, lose nothing (those beyond are
+ * rounded to 53 bits).
  *  q, oq      [B,H,T,D] of `dtype`;  k, ok [B,Hk,T,D], both NULL for one tensor
  *  freqs      [R/2] fp32 device array (la_rotary_frequencies fills a host one)
  *  positions  device int64, [B,T] (positions_per_batch = 1) or [T] (= 0), any

@@ -1,8 +1,9 @@
 // la_rotary.cu -- rotary positions on queries and keys, and the inverse rotation (its gradient).
 //
 // Pair i of a head's first R entries, at position p, turns by the angle p f_i.  The turns
-// p f_i / (2 pi) are formed in double (a position of 2^31 still leaves 2^-21 of a turn's last
-// bit), reduced to [-1/2, 1/2], and only then given to sincospi in fp32.
+// p f_i / (2 pi) are formed as a sum of two doubles, with the products' remainders and the part of
+// 1 / (2 pi) that one double leaves out (one double alone is off by 7e-6 of a radian at positions of
+// 2^35, and says nothing at 2^53), reduced to [-1/2, 1/2], and only then given to sincospi in fp32.
 //
 // Bound by HBM: every element is read and written once.  A thread owns V elements of one token's
 // row (V of each half in the half layout, V / 2 neighbouring pairs interleaved) and walks over the
@@ -17,6 +18,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;          // heads whose elements a thread has on their way at a time
+
+// The turns of frequency f at position p (a whole number of at most 53 bits), in [-1/2, 1/2].
+__device__ __forceinline__ float turns_of(double p, float f) {
+    constexpr double c = 0.15915494309189535, c_rest = -9.839338337591243e-18;     // 1 / (2 pi)
+    const double t = p * (double)f, t_rest = ::fma(p, (double)f, -t);
+    const double hi = t * c, lo = ::fma(t, c, -hi) + ::fma(t, c_rest, t_rest * c);
+    const double r = (hi - rint(hi)) + lo;             // lo: up to 1 where hi has no bits behind the point
+    return (float)(r - rint(r));
+}
 
 // V: elements an access; an interleaved item is at least a pair, of two accesses where V = 1
 // (tensors aligned to one element only).
@@ -41,9 +51,8 @@ rotary_kernel(RotaryArgs a, int items, int heads_per) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const float f = a.freqs[INTER ? item * P + i : c0 + i];
-            const double turns = (double)pos * ((double)f * 0.15915494309189533577);
             float s, c;
-            sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+            sincospif(2.f * turns_of((double)pos, f), &s, &c);
             cs[i] = c * a.magnitude;
             sn[i] = s * a.sign * a.magnitude;
         }

@@ -1,5 +1,7 @@
 """Non-finite values, outlying rows, far positions and narrow accesses of the operators around the
 token mixers, against their 64-bit definitions."""
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -66,3 +68,26 @@ def test_group_norm_variance_behind_an_outlying_first_row(C, G):
         xm = x[b].abs().max().double()
         close(mean[b:b + 1], wm, "mean", 100, xm)
         close(rstd[b:b + 1], wr, "rstd", 200, wr * (1 + wr * xm))
+
+
+# ------------------------------------------------------------------------------------- rotary --
+
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_angles_of_far_positions(layout):
+    """Angles reduced exactly, as fractions, up to the positions that 64-bit numbers hold."""
+    pos = [0, 1, -1, 2 ** 31 + 12345, 2 ** 35 + 1, -(2 ** 40) - 3, 2 ** 45 + 1, 2 ** 52 + 7, 2 ** 53, -(2 ** 53)]
+    rates = torch.tensor([1.0, 0.7498942, 0.3, 1e-3, 1e-7, 3e-12])
+    ang = [[float((Fraction(p) * Fraction(float(f)) / TWO_PI) % 1 * TWO_PI) for f in rates] for p in pos]
+    ang = torch.tensor(ang, dtype=torch.float64, device=_dev())[None, None]
+    q = _gen(6)(1, 2, len(pos), 12)
+    o = torch.full_like(q, NAN)
+    la.la_rotary_fwd(q, None, o, None, rates.to(_dev()), positions=torch.tensor(pos, device=_dev()), layout=layout)
+    a, b = (q[..., :6], q[..., 6:]) if layout == "half" else (q[..., 0::2], q[..., 1::2])
+    a, b = a.double(), b.double()
+    u, v = a * ang.cos() - b * ang.sin(), a * ang.sin() + b * ang.cos()
+    want = torch.cat([u, v], -1) if layout == "half" else torch.stack([u, v], -1).flatten(-2)
+    # the bound of the parity test: the angle off by pi 2^-24, the sine's own 2 roundings, two products, a sum
+    close(o, want, "rotary", 12, 2.5 * q.abs().max().double())
