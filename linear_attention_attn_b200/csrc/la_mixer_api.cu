@@ -36,15 +36,15 @@ la_status check_ws(size_t need, const void *ws, size_t bytes) {
 }
 
 // The tensors of one call: presence, alignment to an element, and that no output overlaps another
-// tensor of the call (in_place: the input that the output may be, exactly).
+// tensor of the call.  in() gives the input's bit; in_place is the inputs that an output may be,
+// exactly (another input at the same address is an overlap: it may be read after the output is written).
 class Tensors {
 public:
     explicit Tensors(bool no_tokens) : no_tokens_(no_tokens) {}
-    void in(const char *name, const void *p, double count, size_t elem, bool optional = false) {
-        add(name, p, count, elem, optional, false, nullptr);
+    unsigned in(const char *name, const void *p, double count, size_t elem, bool optional = false) {
+        return add(name, p, count, elem, optional, false, 0);
     }
-    void out(const char *name, const void *p, double count, size_t elem, bool optional = false,
-             const void *in_place = nullptr) {
+    void out(const char *name, const void *p, double count, size_t elem, bool optional = false, unsigned in_place = 0) {
         add(name, p, count, elem, optional, true, in_place);
     }
     // Presence and alignment, then the workspace (`need` bytes, if any), then the overlaps, the
@@ -57,7 +57,7 @@ public:
             if (!t_[i].out) continue;
             for (int j = 0; j < n_; ++j) {
                 if (j == i || (t_[j].out && j < i)) continue;
-                if (t_[i].p == t_[j].p && t_[i].in_place == (const void *)t_[j].p && t_[i].bytes == t_[j].bytes) continue;
+                if (t_[i].p == t_[j].p && (t_[i].in_place >> j & 1) && t_[i].bytes == t_[j].bytes) continue;
                 if (t_[i].p < t_[j].p + t_[j].bytes && t_[j].p < t_[i].p + t_[i].bytes)
                     return refuse(LA_ERR_INVALID_ARG, "%s overlaps %s", t_[i].name, t_[j].name);
             }
@@ -70,21 +70,23 @@ private:
         const char *name;
         uintptr_t p, bytes;
         bool out;
-        const void *in_place;
+        unsigned in_place;
     };
-    void add(const char *name, const void *p, double count, size_t elem, bool optional, bool out, const void *in_place) {
+    unsigned add(const char *name, const void *p, double count, size_t elem, bool optional, bool out, unsigned in_place) {
         if (!p) {
             if (!optional && !(no_tokens_ && count == 0) && status_ == LA_OK) {
                 status_ = LA_ERR_INVALID_ARG;
                 bad_ = name;
             }
-            return;
+            return 0;
         }
         if (((uintptr_t)p & (elem - 1)) && status_ == LA_OK) {
             status_ = LA_ERR_ALIGNMENT;
             bad_ = name;
         }
-        if (count > 0) t_[n_++] = Tensor{name, (uintptr_t)p, (uintptr_t)(count * elem), out, in_place};
+        if (!(count > 0)) return 0;
+        t_[n_] = Tensor{name, (uintptr_t)p, (uintptr_t)(count * elem), out, in_place};
+        return 1u << n_++;
     }
     Tensor t_[24];
     int n_ = 0;
@@ -163,12 +165,12 @@ la_status rotary_entry(float sign, const void *q, const void *k, void *oq, void 
     const double n = (double)B * T * D;
     const size_t es = elem_bytes(dt);
     Tensors t(T == 0);
-    t.in(sign > 0 ? "q" : "doq", q, n * H, es);
-    if (two) t.in(sign > 0 ? "k" : "dok", k, n * Hk, es);
+    const unsigned q_bit = t.in(sign > 0 ? "q" : "doq", q, n * H, es);
+    const unsigned k_bit = two ? t.in(sign > 0 ? "k" : "dok", k, n * Hk, es) : 0;
     t.in("freqs", freqs, R / 2, 4);
     t.in("positions", positions, (double)T * (per_batch ? B : 1), 8, true);
-    t.out(sign > 0 ? "oq" : "dq", oq, n * H, es, false, q);
-    if (two) t.out(sign > 0 ? "ok" : "dk", ok, n * Hk, es, false, k);
+    t.out(sign > 0 ? "oq" : "dq", oq, n * H, es, false, q_bit);
+    if (two) t.out(sign > 0 ? "ok" : "dk", ok, n * Hk, es, false, k_bit);
     LA_TRY(t.check());
     if (T == 0) return LA_OK;
     return rotary(RotaryArgs{q, k, oq, ok, freqs, positions, start, per_batch, B, H, Hk, T, D, R,
@@ -186,10 +188,10 @@ la_status conv_fwd_entry(const void *x, const float *w, const float *bias, const
     t.in("x", x, n, es);
     t.in("w", w, (double)C * W, 4);
     t.in("bias", bias, C, 4, true);
-    t.in("state_in", state_in, st, es, !step);
+    const unsigned state = t.in("state_in", state_in, st, es, !step);
     t.in("lengths", lengths, B, 4, true);
     t.out("y", y, n, es);
-    t.out("state_out", state_out, st, es, !step, state_in);
+    t.out("state_out", state_out, st, es, !step, state);
     LA_TRY(t.check());
     if (T == 0) return pass_on(state_out, state_in, (size_t)st * es, (cudaStream_t)stream);
     ConvArgs a = {};
@@ -215,10 +217,10 @@ la_status scan_fwd_entry(bool step, const void *x, const void *dt, const float *
     t.in("D", D, C, 4, true);
     t.in("z", z, n, es, true);
     t.in("dt_bias", dt_bias, C, 4, true);
-    t.in("state_in", state_in, st, 4, !step);
+    const unsigned state = t.in("state_in", state_in, st, 4, !step);
     t.in("lengths", lengths, B, 4, true);
     t.out("y", y, n, es);
-    t.out("state_out", state_out, st, 4, !step, state_in);
+    t.out("state_out", state_out, st, 4, !step, state);
     const size_t need = step ? 0 : need_for(LA_OP_SELECTIVE_SCAN_FWD, B, T, C, G, N, dtype);
     LA_TRY(t.check(need, ws, ws_bytes));
     if (T == 0) return pass_on(state_out, state_in, (size_t)st * 4, (cudaStream_t)stream);
@@ -411,10 +413,10 @@ la_status la_group_norm_fwd(const void *x, const float *gamma, const float *beta
     const double n = (double)B * T * C, bg = (double)B * G;
     const size_t need = need_for(LA_OP_GROUP_NORM_FWD, B, T, C, G, 1, dtype);
     Tensors t(T == 0);
-    t.in("x", x, n, es);
+    const unsigned x_bit = t.in("x", x, n, es);
     t.in("gamma", gamma, C, 4, true);
     t.in("beta", beta, C, 4, true);
-    t.out("y", y, n, es, false, x);
+    t.out("y", y, n, es, false, x_bit);
     t.out("mean", mean, bg, 4, true);
     t.out("rstd", rstd, bg, 4, true);
     LA_TRY(t.check(need, workspace, workspace_bytes));
@@ -437,13 +439,14 @@ la_status la_group_norm_bwd(const void *x, const void *dy, const float *mean, co
     const double n = (double)B * T * C, bg = (double)B * G;
     const size_t need = need_for(LA_OP_GROUP_NORM_BWD, B, T, C, G, 1, dtype);
     Tensors t(T == 0);
-    t.in("x", x, n, es);
-    t.in("dy", dy, n, es);
+    // every element of x and dy is read by the thread that writes it in dx, and the sums are done by
+    // then: dx may be dy, also where dy is x
+    const unsigned x_bit = t.in("x", x, n, es), dy_bit = t.in("dy", dy, n, es);
     t.in("mean", mean, bg, 4);
     t.in("rstd", rstd, bg, 4);
     t.in("gamma", gamma, C, 4, true);
     t.in("beta", beta, C, 4, true);
-    t.out("dx", dx, n, es, false, dy);
+    t.out("dx", dx, n, es, false, dy_bit | (x == dy ? x_bit : 0));
     t.out("dgamma", dgamma, C, 4, true);
     t.out("dbeta", dbeta, C, 4, true);
     LA_TRY(t.check(need, workspace, workspace_bytes));
