@@ -189,7 +189,7 @@ __device__ __forceinline__ void bwd_tokens(const ConvArgs &a, const Raw<T, V> (&
 #pragma unroll
         for (int i = 0; i < L::n; ++i) {
             if (!INNER && t >= n) g.e[i] = L::splat(0.f);
-            if (INNER || t < t1) {
+            if (INNER || (t < t1 && t < n)) {
                 db.e[i] = add(db.e[i], g.e[i]);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) dw[j].e[i] = fma(g.e[i], win[j].e[i], dw[j].e[i]);
@@ -198,13 +198,15 @@ __device__ __forceinline__ void bwd_tokens(const ConvArgs &a, const Raw<T, V> (&
         }
         const int u = t - (W - 1);
         if (INNER || (u < t1 && (u >= t0 || (t0 == 0 && dfirst)))) {
-            // dx[u] = sum_k w[W-1-k] g[u+k]: g[u] is the oldest in the window
+            // dx[u] = sum_k w[W-1-k] g[u+k]: g[u] is the oldest in the window.  Only tokens that exist take
+            // part (a tap may be infinite, and its product with a zero no zero).
             L d;
 #pragma unroll
             for (int i = 0; i < L::n; ++i) {
-                d.e[i] = mul(w[0].e[i], g.e[i]);
+                d.e[i] = INNER || t < n ? mul(w[0].e[i], g.e[i]) : L::splat(0.f);
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) d.e[i] = fma(w[W - 1 - j].e[i], gw[j].e[i], d.e[i]);
+                for (int j = 0; j < W - 1; ++j)
+                    if (INNER || (u + j >= 0 && u + j < n)) d.e[i] = fma(w[W - 1 - j].e[i], gw[j].e[i], d.e[i]);
             }
             if (INNER) {
                 store_lanes<V>(dx + u * C, d);

@@ -91,3 +91,47 @@ def test_rotary_angles_of_far_positions(layout):
     want = torch.cat([u, v], -1) if layout == "half" else torch.stack([u, v], -1).flatten(-2)
     # the bound of the parity test: the angle off by pi 2^-24, the sine's own 2 roundings, two products, a sum
     close(o, want, "rotary", 12, 2.5 * q.abs().max().double())
+
+
+# ------------------------------------------------------------------------------- convolution --
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [2, 4, 7])
+def test_short_conv_rows_behind_the_end_take_no_part(dtype, W):
+    """An infinite last row (its gradient 0 behind it times infinity is no term of dw), and channels with
+    infinite or NaN taps, whose rows behind the end still come out as zeros."""
+    normal = _gen(7)
+    dt = DTYPES[dtype]
+    B, T, C = 4, 40, 12
+    x, dy, w = normal(B, T, C, dtype=dt), normal(B, T, C, dtype=dt), normal(C, W)
+    lengths = torch.tensor([T, 21, 0, 1], dtype=torch.int32, device=_dev())
+    ends = lengths.tolist()
+    s, ds = normal(B, W - 1, C, dtype=dt), normal(B, W - 1, C, dtype=dt)
+    for b, n in enumerate(ends):
+        x[b, n:], dy[b, n:] = NAN, NAN
+        if n:
+            x[b, n - 1, 3] = INF
+    w[5, W - 1], w[6, 0], w[7, W // 2] = INF, NAN, -INF
+    y = torch.full_like(x, NAN)
+    la.la_short_conv_fwd(x, w, y, state_in=s, lengths=lengths, activation="none")
+    dx, dw, dso = torch.full_like(x, NAN), torch.full_like(w, NAN), torch.full_like(s, NAN)
+    la.la_short_conv_bwd(x, w, dy, dx, dw, state_in=s, dstate_in=ds, dstate_out=dso, lengths=lengths,
+                         activation="none")
+    # the formula, token by token
+    wdw = torch.zeros(C, W, dtype=torch.float64, device=_dev())
+    wdx = torch.zeros(B, T, C, dtype=torch.float64, device=_dev())
+    wds = torch.zeros(B, W - 1, C, dtype=torch.float64, device=_dev())
+    w64 = w.double()
+    for b, n in enumerate(ends):
+        e = torch.cat([s[b], x[b, :n]]).double()
+        de = torch.zeros_like(e)
+        for t in range(n):
+            for j in range(W):
+                wdw[:, j] += dy[b, t].double() * e[t + j]
+                de[t + j] += dy[b, t].double() * w64[:, j]
+        de[n:] += ds[b].double()
+        wds[b], wdx[b, :n] = de[:W - 1], de[W - 1:]
+        assert torch.equal(y[b, n:], torch.zeros_like(y[b, n:]))
+    for name, got, want in (("dx", dx, wdx), ("dw", dw, wdw), ("dstate_out", dso, wds)):
+        ok = _same_where_not_finite(got, want, name)
+        close(got[ok], want[ok], name, 4 * W + 64 + B * T, 200.0)
