@@ -526,9 +526,10 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                 const bool in_seq = t < n;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    f2 dx = fma2(d2[j], q2[j], mul2(Dc[j], g2[j]));
+                    // without D no product with a zero: x or dy may be infinite
+                    f2 dx = a.D ? fma2(d2[j], q2[j], mul2(Dc[j], g2[j])) : mul2(d2[j], q2[j]);
                     f2 dt = mul2(fma2(x2[j], q2[j], mul2(ap2[j], both(1.f / kLog2e))), sg2[j]);
-                    f2 gz = mul2(dz2[j], fma2(Dc[j], x2[j], y2[j]));
+                    f2 gz = mul2(dz2[j], a.D ? fma2(Dc[j], x2[j], y2[j]) : y2[j]);
                     if (!in_seq) dx = dt = gz = 0;
                     dD[j] = fma2(g2[j], x2[j], dD[j]);                    // 0 behind the end: g and x are
                     dbias[j] = add2(dbias[j], dt);

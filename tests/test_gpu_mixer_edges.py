@@ -135,3 +135,80 @@ def test_short_conv_rows_behind_the_end_take_no_part(dtype, W):
     for name, got, want in (("dx", dx, wdx), ("dw", dw, wdw), ("dstate_out", dso, wds)):
         ok = _same_where_not_finite(got, want, name)
         close(got[ok], want[ok], name, 4 * W + 64 + B * T, 200.0)
+
+
+# -------------------------------------------------------------------------------------- scan --
+
+ORDER = ("x", "dt", "A", "Bm", "Cm", "D", "z", "dt_bias", "state_in")
+
+
+def _infinite_case(dtype, N, what, skip, gate, T=21, seed=8):
+    """One channel in three meets an infinite x or dt in the middle; x, B, C and the state positive, so that
+    the formula's sums are of one sign."""
+    normal = _gen(seed)
+    dt = DTYPES[dtype]
+    B, C = 2, 12
+    c = dict(x=normal(B, T, C, dtype=dt).abs(), dt=normal(B, T, C, dtype=dt, scale=0.5), A=-torch.exp(normal(C, N)),
+             Bm=normal(B, T, 1, N, dtype=dt).abs() + 0.5, Cm=normal(B, T, 1, N, dtype=dt).abs() + 0.5,
+             D=normal(C).abs() if skip else None, z=normal(B, T, C, dtype=dt).abs() if gate else None, dt_bias=None,
+             state_in=normal(B, C, N).abs())
+    c[what][:, 9, ::3] = INF
+    return c
+
+
+def _formula_gradients(c, dy):
+    """The gradients' formulas written out (automatic differentiation multiplies by zeros of its own)."""
+    v = {n: None if t is None else t.double() for n, t in c.items()}
+    x, A, z, D = v["x"], v["A"], v["z"], v["D"]
+    B, T, C = x.shape
+    r = v["dt"]
+    d = torch.logaddexp(r, torch.zeros_like(r))
+    sg = None if z is None else torch.special.expit(z)
+    dy = dy.double()
+    e = dy if z is None else dy * (z * sg)
+    hs, h = [v["state_in"]], v["state_in"]
+    for t in range(T):
+        h = torch.exp(d[:, t, :, None] * A) * h + (d[:, t] * x[:, t])[..., None] * v["Bm"][:, t]
+        hs.append(h)
+    g = {n: torch.zeros_like(v[n]) for n in ORDER if v[n] is not None}
+    w = torch.zeros_like(h)
+    for t in reversed(range(T)):
+        a = torch.exp(d[:, t, :, None] * A)
+        lam = e[:, t, :, None] * v["Cm"][:, t] + w
+        g["Cm"][:, t, 0] = (e[:, t, :, None] * hs[t + 1]).sum(1)
+        g["Bm"][:, t, 0] = ((d[:, t] * x[:, t])[..., None] * lam).sum(1)
+        q = (lam * v["Bm"][:, t]).sum(-1)
+        w = a * lam
+        p = w * hs[t]
+        g["x"][:, t] = d[:, t] * q if D is None else d[:, t] * q + D * e[:, t]
+        g["dt"][:, t] = (x[:, t] * q + (A * p).sum(-1)) * torch.special.expit(r[:, t])
+        g["A"] += (d[:, t, :, None] * p).sum(0)
+        if D is not None:
+            g["D"] += (e[:, t] * x[:, t]).sum(0)
+        if z is not None:
+            y = (hs[t + 1] * v["Cm"][:, t]).sum(-1)
+            y = y if D is None else y + D * x[:, t]
+            g["z"][:, t] = dy[:, t] * y * (sg[:, t] * (1 + z[:, t] * (1 - sg[:, t])))
+    g["state_in"] = w
+    return g
+
+
+@pytest.mark.parametrize("N", [4, 16, 64])
+@pytest.mark.parametrize("skip,gate", [(False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("T", [24])
+def test_selective_scan_gradient_of_infinities(T, N, skip, gate):
+    """An infinite incoming gradient at one token of some channels, and an infinite x at the last one."""
+    c = _infinite_case("f32", N, "x", skip, gate, T)
+    c["x"] = torch.where(torch.isinf(c["x"]), torch.ones_like(c["x"]), c["x"])
+    c["x"][:, -1, 1::3] = INF
+    dy = _gen(9)(*c["x"].shape).abs()
+    dy[:, 9, ::3] = INF
+    got = {n: torch.full_like(c[n], 7.0) for n in ORDER if c[n] is not None}
+    la.la_selective_scan_bwd(c["x"], c["dt"], c["A"], c["Bm"], c["Cm"], dy, got["x"], got["dt"], got["A"], got["Bm"],
+                             got["Cm"], D=c["D"], dD=got.get("D"), z=c["z"], dz=got.get("z"),
+                             state_in=c["state_in"], dstate_out=got["state_in"])
+    want = _formula_gradients(c, dy)
+    for n in got:
+        ok = _same_where_not_finite(got[n], want[n], "d" + n)
+        scale = want[n][ok].abs().max() if ok.any() else 1.0
+        close(got[n][ok], want[n][ok], "d" + n, 2 * (24 * dy.shape[1] + 64) + dy.numel(), scale)
