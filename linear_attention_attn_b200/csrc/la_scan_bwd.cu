@@ -255,6 +255,34 @@ struct Four {
     }
 };
 
+// dA's sum over the `count` tokens of a tile that exist, one by one: hs is the state before them, w the
+// gradient that the tokens behind them hand over.
+__device__ __forceinline__ void last_tokens(int count, const float *d, const float *u, const float *e, int width,
+                                            const float *B, const float *C, int NP, const f2 (&A2)[2],
+                                            const f2 (&hs)[2], f2 w0, f2 w1, float (&dA)[kNS]) {
+    f2 w[2] = {w0, w1}, sum[2] = {0, 0};
+#pragma unroll 1
+    for (int j = count - 1; j >= 0; --j) {
+        f2 h[2] = {hs[0], hs[1]};
+#pragma unroll 1
+        for (int i = 0; i < j; ++i) {
+            const f2 di = both(d[i * width]), ui = both(u[i * width]);
+            const Four Bi(B + i * NP);
+            h[0] = fma2(decay2(di, A2[0]), h[0], mul2(ui, Bi.v[0]));
+            h[1] = fma2(decay2(di, A2[1]), h[1], mul2(ui, Bi.v[1]));
+        }
+        const f2 dj = both(d[j * width]), ej = both(e[j * width]);
+        const Four Cj(C + j * NP);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            w[k] = mul2(decay2(dj, A2[k]), fma2(ej, Cj.v[k], w[k]));
+            sum[k] = fma2(dj, mul2(w[k], h[k]), sum[k]);
+        }
+    }
+    unpack2(sum[0], dA[0], dA[1]);
+    unpack2(sum[1], dA[2], dA[3]);
+}
+
 // First launch of the segmented form: (S, R, sum of d) of every segment.
 template <typename T, int LN>
 __global__ void __launch_bounds__(Cfg<LN>::threads)
@@ -426,6 +454,18 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
         stg.store(t0 + (count - 1) * kTile, s, (count - 1) & 1);
     }
     __syncthreads();
+    // Where the sequence ends within a sub-tile, the tile's sum for dA takes the tokens that exist one by one and
+    // waits in the workspace (kept in registers over the loop, or as a test for each token, it spills and costs
+    // up to 10 % at N = 5 .. 8 and N > 32): behind them d is 0, but the state may be infinite.
+    if (count > 0 && (n - t0) % kSub != 0) {
+        const int buf = (count - 1) & 1, at = buf * K::pairs + ch, bt = buf * kTile * K::NP + n0;
+        copy_wait<0>();
+        const ulonglong2 hs = *reinterpret_cast<const ulonglong2 *>(s.before + buf * K::subs * K::threads + tid);
+        float v[kNS];
+        last_tokens((n - t0 - 1) % kTile + 1, s.d + at, s.u + at, s.e + at, K::width, s.B + bt, s.C + bt, K::NP, A2,
+                    {hs.x, hs.y}, w[0], w[1], v);
+        if (live) store_states(sg.pA + (((long long)p.b * sg.segs + p.seg) * a.C + c) * a.N, n0, a.N, v);
+    }
     for (int tile = count - 1; tile >= 0; --tile) {
         const int buf = tile & 1, tb = t0 + tile * kTile;
         copy_wait<0>();
@@ -507,6 +547,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
             sum_channels<LN>(rc, rb, s.columns + warp * Columns<LN>::bytes, lane,
                              s.red + (warp * kTile + sub * kSub) * 2 * K::NP);
         }
+        if (n - tb <= kTile && (n & (kSub - 1))) dA[0] = dA[1] = 0;              // waits in the workspace
         if (tile > 0) stg.store(tb - kTile, s, buf ^ 1);
         __syncthreads();
 #pragma unroll
@@ -580,6 +621,12 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
         float v[4];
         unpack2(dA[0], v[0], v[1]);
         unpack2(dA[1], v[2], v[3]);
+        if (count > 0 && (n - t0) % kSub != 0) {
+            float last[kNS];
+            load_states(sg.pA + (part * a.C + c) * a.N, n0, a.N, last);
+#pragma unroll
+            for (int k = 0; k < kNS; ++k) v[k] += last[k];
+        }
         store_states(sg.pA + (part * a.C + c) * a.N, n0, a.N, v);
         unpack2(w[0], v[0], v[1]);
         unpack2(w[1], v[2], v[3]);

@@ -195,7 +195,7 @@ def _formula_gradients(c, dy):
 
 @pytest.mark.parametrize("N", [4, 16, 64])
 @pytest.mark.parametrize("skip,gate", [(False, True), (True, False), (False, False)])
-@pytest.mark.parametrize("T", [24])
+@pytest.mark.parametrize("T", [24, 21])
 def test_selective_scan_gradient_of_infinities(T, N, skip, gate):
     """An infinite incoming gradient at one token of some channels, and an infinite x at the last one."""
     c = _infinite_case("f32", N, "x", skip, gate, T)
