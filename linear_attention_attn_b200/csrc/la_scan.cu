@@ -36,6 +36,12 @@ template <int LN> struct Cfg {
     static constexpr int per = (quads + kThreads - 1) / kThreads;
     static constexpr int bquads = kTile * LN;               // 4 states of a token's B (or C)
     static constexpr int bper = (bquads + kThreads - 1) / kThreads;
+    // Blocks an SM that the kernels for padded states are held to.  They keep more in registers; without a
+    // bound N = 6 bf16 came to 138 and 225 us (B8 T2048 C1024; 168 with no state kept at 0), held to 128
+    // registers 179 us.  One and four lanes (N < 4, 9 .. 16) take what they like: N = 12 bf16 186 us, 234 held.
+    template <typename T> static constexpr int fit() {
+        return LN == 1 || LN == 4 ? 1 : sizeof(T) == 4 ? (LN == 8 ? 8 : 6) : (LN == 8 ? 10 : 8);
+    }
     static constexpr size_t smem = sizeof(float) * (6 * pairs + 2 * 2 * kTile * kNS * LN);
 };
 
@@ -46,7 +52,7 @@ struct Seg {
 };
 
 // Tokens [t0, t1) of the block's channels from state h.  FULL: with outputs; else only h and sum of d.
-template <typename T, int LN, bool FULL>
+template <typename T, int LN, bool FULL, bool PAD>
 __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Place &p, int t0, int t1,
                                      const f2 (&A2)[2], f2 (&h)[2], float &sum, float *smem) {
     using K = Cfg<LN>;
@@ -64,6 +70,7 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
     constexpr int row = K::width / 4, t_step = kThreads / row, b_step = kThreads / LN;
     static_assert(kThreads % row == 0, "");
     const int c = tid % row * 4, have = p.nc - c, t_first = tid / row;
+    const Existing<PAD && FULL> real(nl * kNS, a.N);          // (without sums padded states meet no others)
     const int m = tid % LN * 4, b_have = a.N - m, b_first = tid / LN;
     const long long x0 = (row0 + t_first) * a.C + p.c0 + c, xs = (long long)t_step * a.C;
     const long long b0 = ((row0 + b_first) * a.G + p.g) * a.N + m, bs = (long long)b_step * a.G * a.N;
@@ -158,8 +165,8 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
                 const float d1 = pd[(q + j) * K::width];
                 const f2 d = both(d1), u = both(pu[(q + j) * K::width]);
                 const ulonglong2 B = pB[(q + j) * LN];
-                h[0] = fma2(decay2(d, A2[0]), h[0], mul2(u, B.x));
-                h[1] = fma2(decay2(d, A2[1]), h[1], mul2(u, B.y));
+                h[0] = real(fma2(decay2(d, A2[0]), h[0], mul2(u, B.x)), 0);
+                h[1] = real(fma2(decay2(d, A2[1]), h[1], mul2(u, B.y)), 1);
                 if (FULL) {
                     const ulonglong2 C = pC[(q + j) * LN];
                     float y0, y1;
@@ -221,10 +228,13 @@ __device__ __forceinline__ void walk(const ScanArgs &a, const Seg &sg, const Pla
         }
 }
 
+// PAD: N does not fill its lanes (see Existing).  Against padded states left to themselves, at B8 T2048 C1024 and
+// N = 1, 6, 12, 30, 50: bf16 171, 179, 186, 453, 1321 us instead of 179, 167, 205, 445, 1280; f32 169, 214, 188, 335,
+// 952 instead of 173, 192, 191, 311, 846.
 // PASS 0: whole sequences.  PASS 1: segment 0 in full, segments 1 .. segs - 2 for (S, sum).
 // PASS 2: segments 1 .. segs - 1 in full.
-template <typename T, int LN, int PASS>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int LN, int PASS, bool PAD>
+__global__ void __launch_bounds__(kThreads, PAD ? Cfg<LN>::template fit<T>() : 0)
 scan_fwd_kernel(ScanArgs a, Seg sg, int tiles) {
     using K = Cfg<LN>;
     extern __shared__ float4 smem4[];
@@ -263,9 +273,9 @@ scan_fwd_kernel(ScanArgs a, Seg sg, int tiles) {
     const f2 A2[2] = {pack2(A4[0], A4[1]), pack2(A4[2], A4[3])};
     f2 h[2] = {pack2(h4[0], h4[1]), pack2(h4[2], h4[3])};
     if (PASS != 1 || p.seg == 0)
-        walk<T, LN, true>(a, sg, p, t0, t1, A2, h, sum, smem);
+        walk<T, LN, true, PAD>(a, sg, p, t0, t1, A2, h, sum, smem);
     else
-        walk<T, LN, false>(a, sg, p, t0, t1, A2, h, sum, smem);
+        walk<T, LN, false, PAD>(a, sg, p, t0, t1, A2, h, sum, smem);
     if (!live) return;
     unpack2(h[0], h4[0], h4[1]);
     unpack2(h[1], h4[2], h4[3]);
@@ -289,6 +299,7 @@ scan_step_kernel(ScanArgs a, int vec, int bvec) {
     constexpr int S = 32 / LN, own = Kept<LN>::value;
     const int lane = threadIdx.x & 31, nl = lane_states<LN>(), n0 = nl * kNS, r0 = first_token<LN>(nl);
     const int c = blockIdx.x * (kStepThreads / LN) + lane_channel<LN>(), b0 = blockIdx.y * 4;
+    const Existing<true> real(n0, a.N);
     const bool live = c < a.C;
     const int rows = live ? min(4, a.B - b0) : 0;
     const int g = a.G == 1 || !live ? 0 : c / (a.C / a.G);
@@ -340,7 +351,7 @@ scan_step_kernel(ScanArgs a, int vec, int bvec) {
         Bq[r].values(B);
         Cq[r].values(C);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) s[k] = fma2(decay2(both(d), A2[k]), s[k], mul2(both(u), B[k]));
+        for (int k = 0; k < 2; ++k) s[k] = real(fma2(decay2(both(d), A2[k]), s[k], mul2(both(u), B[k])), k);
         float y0, y1;
         unpack2(fma2(C[0], s[0], mul2(C[1], s[1])), y0, y1);
         sum[r] = y0 + y1;
@@ -385,8 +396,8 @@ void fwd_segments(int B, int T, int C, int G, int N, int *segs, int *len) {
     *segs = (T + *len - 1) / *len;
 }
 
-template <typename T, int LN>
-la_status fwd_ln(const ScanArgs &a, cudaStream_t st) {
+template <typename T, int LN, bool PAD>
+la_status fwd_pad(const ScanArgs &a, cudaStream_t st) {
     using K = Cfg<LN>;
     Seg sg;
     fwd_segments(a.B, a.T, a.C, a.G, a.N, &sg.segs, &sg.len);
@@ -397,13 +408,19 @@ la_status fwd_ln(const ScanArgs &a, cudaStream_t st) {
     const int tiles = (a.C / a.G + K::width - 1) / K::width;
     const unsigned blocks = (unsigned)((long long)a.B * a.G * tiles);
     if (sg.segs == 1)
-        return launch("selective_scan_fwd", scan_fwd_kernel<T, LN, 0>, dim3(blocks), dim3(kThreads), K::smem, st, a,
-                      sg, tiles);
+        return launch("selective_scan_fwd", scan_fwd_kernel<T, LN, 0, PAD>, dim3(blocks), dim3(kThreads), K::smem, st,
+                      a, sg, tiles);
     const dim3 grid(blocks * (sg.segs - 1));
-    la_status rc = launch("selective_scan_fwd_ends", scan_fwd_kernel<T, LN, 1>, grid, dim3(kThreads), K::smem, st, a,
-                          sg, tiles);
+    la_status rc = launch("selective_scan_fwd_ends", scan_fwd_kernel<T, LN, 1, PAD>, grid, dim3(kThreads), K::smem, st,
+                          a, sg, tiles);
     if (rc != LA_OK) return rc;
-    return launch_pdl("selective_scan_fwd", scan_fwd_kernel<T, LN, 2>, grid, dim3(kThreads), K::smem, st, a, sg, tiles);
+    return launch_pdl("selective_scan_fwd", scan_fwd_kernel<T, LN, 2, PAD>, grid, dim3(kThreads), K::smem, st, a, sg,
+                      tiles);
+}
+
+template <typename T, int LN>
+la_status fwd_ln(const ScanArgs &a, cudaStream_t st) {
+    return a.N == kNS * LN ? fwd_pad<T, LN, false>(a, st) : fwd_pad<T, LN, true>(a, st);
 }
 
 template <typename T>

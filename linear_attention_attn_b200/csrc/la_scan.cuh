@@ -1,7 +1,7 @@
 // la_scan.cuh -- layout shared by the forward, step and backward kernels of the selective scan.
 //
 // A channel's N states are spread over LN lanes of a warp, kNS = 4 each (N is padded to 4 LN with
-// rates and projections of zero, which contribute nothing), so sums over n are log2(LN) shuffles and
+// rates and projections of zero, which contribute nothing, see Existing), so sums over n are log2(LN) shuffles and
 // a warp works on S = 32 / LN channels.  Lane l has states 4 (l / S) on of channel l % S: lanes that
 // read the same B and C are neighbours, and a 16-byte read of shared memory whose neighbours agree
 // takes 2 passes instead of 4 (measured; 8 bytes: 1 instead of 2), while the reads that differ from
@@ -60,6 +60,20 @@ template <int LN> __device__ __forceinline__ int lane_states() { return (threadI
 template <int LN> __device__ __forceinline__ int lane_channel() {
     return (threadIdx.x >> 5) * (32 / LN) + (threadIdx.x & 31) % (32 / LN);
 }
+
+// Keeps the states that exist of a lane's four and makes the others 0.  Padded states have rates and
+// projections of 0, but with an infinite step or input 0 times infinity would come to be among them, and
+// the channel's sum NaN.  Only kernels for an N that does not fill its lanes (PAD) have to.
+template <bool PAD> struct Existing {
+    f2 mask[2];
+    __device__ __forceinline__ Existing(int n0, int N) {
+        if (PAD)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                mask[k] = (n0 + 2 * k < N ? 0xffffffffull : 0) | (n0 + 2 * k + 1 < N ? 0xffffffffull << 32 : 0);
+    }
+    __device__ __forceinline__ f2 operator()(f2 v, int k) const { return PAD ? v & mask[k] : v; }
+};
 
 // Sums v[0..3] (four tokens) over the LN lanes of a channel.  Each step hands half of the values
 // to the partner lane: afterwards lane nl holds the sums of tokens first_token(nl) ..

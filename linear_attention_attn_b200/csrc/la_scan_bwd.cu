@@ -338,7 +338,7 @@ scan_bwd_ends(ScanArgs a, Seg sg, int tiles) {
     if (nl == 0) sg.sum[at] = sum;
 }
 
-template <typename T, int LN>
+template <typename T, int LN, bool PAD>
 __global__ void __launch_bounds__(Cfg<LN>::threads)
 scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
     using K = Cfg<LN>;
@@ -431,6 +431,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
 
     // ---- backwards
     const bool gated = a.z != nullptr;
+    const Existing<PAD> real(n0, a.N);
     f2 dA[2] = {0, 0}, dD[2] = {0, 0}, dbias[2] = {0, 0}, Dc[2];
     Stager<T, LN, true> stg(a, sg, p, n);
     {
@@ -479,7 +480,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
             const int at = buf * K::pairs + sub * kSub * K::width + ch, bt = (buf * kTile + sub * kSub) * K::NP + n0;
             const ulonglong2 before =
                 *reinterpret_cast<const ulonglong2 *>(s.before + (buf * K::subs + sub) * K::threads + tid);
-            const f2 hs[2] = {before.x, before.y};
+            const f2 hs[2] = {real(before.x, 0), real(before.y, 1)};
             f2 H[kSub][2], E[kSub][2];
             float ys[kSub / 4][4], lb[kSub / 4][4], dd[kSub / 4][4];
             f2 rc[kSub][2], rb[kSub][2];
@@ -489,8 +490,8 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                 const Four B(s.B + bt + j * K::NP);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    E[j][k] = decay2(d, A2[k]);
-                    H[j][k] = fma2(E[j][k], j ? H[j - 1][k] : hs[k], mul2(u, B.v[k]));
+                    E[j][k] = real(decay2(d, A2[k]), k);
+                    H[j][k] = real(fma2(E[j][k], j ? H[j - 1][k] : hs[k], mul2(u, B.v[k])), k);
                 }
                 if (gated) {
                     const Four C(s.C + bt + j * K::NP);
@@ -511,7 +512,7 @@ scan_bwd_kernel(ScanArgs a, Seg sg, int tiles) {
                 f2 ql[2], qa[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const f2 lam = fma2(e, C.v[k], w[k]);
+                    const f2 lam = real(fma2(e, C.v[k], w[k]), k);
                     rc[j][k] = mul2(e, H[j][k]);
                     rb[j][k] = mul2(u, lam);
                     ql[k] = mul2(lam, B.v[k]);
@@ -734,8 +735,8 @@ size_t layout(int B, int T, int C, int G, int N, void *ws, Seg *sg) {
     return (size_t)(p - (char *)ws);
 }
 
-template <typename T, int LN>
-la_status bwd_ln(const ScanArgs &a, cudaStream_t st) {
+template <typename T, int LN, bool PAD>
+la_status bwd_pad(const ScanArgs &a, cudaStream_t st) {
     using K = Cfg<LN>;
     Seg sg;
     layout(a.B, a.T, a.C, a.G, a.N, a.ws, &sg);
@@ -748,12 +749,17 @@ la_status bwd_ln(const ScanArgs &a, cudaStream_t st) {
         rc = launch("selective_scan_bwd_ends", scan_bwd_ends<T, LN>, grid, block, K::smem, st, a, sg, tiles);
         if (rc != LA_OK) return rc;
     }
-    rc = launch_pdl("selective_scan_bwd", scan_bwd_kernel<T, LN>, grid, block, K::smem, st, a, sg, tiles);
+    rc = launch_pdl("selective_scan_bwd", scan_bwd_kernel<T, LN, PAD>, grid, block, K::smem, st, a, sg, tiles);
     if (rc != LA_OK) return rc;
     const long long plane = (long long)a.B * a.T * a.G * a.N, rest = (long long)a.C * (a.N + 2);
     const int bc_blocks = (int)((plane + 31) / 32);
     return launch_pdl("selective_scan_bwd_join", scan_bwd_join<T>, dim3((unsigned)(bc_blocks + (rest + kJoin - 1) / kJoin)),
                   dim3(kJoin), 0, st, a, sg, tiles, bc_blocks);
+}
+
+template <typename T, int LN>
+la_status bwd_ln(const ScanArgs &a, cudaStream_t st) {
+    return a.N == kNS * LN ? bwd_pad<T, LN, false>(a, st) : bwd_pad<T, LN, true>(a, st);
 }
 
 template <typename T>

@@ -156,6 +156,37 @@ def _infinite_case(dtype, N, what, skip, gate, T=21, seed=8):
     return c
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 9, 16, 18, 33, 64])
+@pytest.mark.parametrize("what", ["x", "dt"])
+@pytest.mark.parametrize("skip,gate", [(False, True), (True, False)])
+def test_selective_scan_infinities_meet_no_padding(dtype, N, what, skip, gate):
+    """Infinite inputs give NaN only where the formula does, whatever the number of states."""
+    c = _infinite_case(dtype, N, what, skip, gate)
+    B, T, C = c["x"].shape
+    leaves = {n: None if c[n] is None else c[n].double().requires_grad_() for n in ORDER}
+    wy, wh = ref.scan(*(leaves[n] for n in ORDER), None, True)
+    y, so = torch.full_like(c["x"], 7.0), torch.full_like(c["state_in"], 7.0)
+    opt = dict(D=c["D"], z=c["z"], state_in=c["state_in"])
+    la.la_selective_scan_fwd(c["x"], c["dt"], c["A"], c["Bm"], c["Cm"], y, state_out=so, **opt)
+    assert not torch.isnan(wy).any() and torch.isinf(wy).any()
+    for name, got, want in (("y", y, wy.detach()), ("state_out", so, wh.detach())):
+        ok = _same_where_not_finite(got, want, name)
+        close(got[ok], want[ok], name, 24 * T + 64)
+    # the single token
+    h, h2 = c["state_in"].double(), c["state_in"].clone()
+    for t in (8, 9, 10):
+        one = {n: c[n][:, t:t + 1].contiguous() for n in ("x", "dt", "Bm", "Cm", "z") if c[n] is not None}
+        wy1, h = ref.scan(*(one[n].double() if n in one else None if c[n] is None else h if n == "state_in"
+                            else c[n].double() for n in ORDER), None, True)
+        tok = {n: v[:, 0].contiguous() for n, v in one.items()}
+        y1 = torch.empty_like(tok["x"])
+        la.la_selective_scan_step(tok["x"], tok["dt"], c["A"], tok["Bm"], tok["Cm"], y1, h2, D=c["D"], z=tok.get("z"))
+        for name, got, want in (("step y", y1, wy1[:, 0]), ("step state", h2, h)):
+            ok = _same_where_not_finite(got, want, name)
+            close(got[ok], want[ok], name, 400)
+
+
 def _formula_gradients(c, dy):
     """The gradients' formulas written out (automatic differentiation multiplies by zeros of its own)."""
     v = {n: None if t is None else t.double() for n, t in c.items()}
@@ -193,7 +224,7 @@ def _formula_gradients(c, dy):
     return g
 
 
-@pytest.mark.parametrize("N", [4, 16, 64])
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 9, 16, 18, 33, 64])
 @pytest.mark.parametrize("skip,gate", [(False, True), (True, False), (False, False)])
 @pytest.mark.parametrize("T", [24, 21])
 def test_selective_scan_gradient_of_infinities(T, N, skip, gate):
