@@ -245,13 +245,13 @@ scan_fwd_kernel(ScanArgs a, Seg sg, int tiles) {
     const bool live = ch < p.nc;
     const long long c = p.c0 + ch;
     float A4[kNS] = {}, h4[kNS] = {};
+    if (PASS == 2) wait_for_stream();
     if (live) {
         load_states(a.A + c * a.N, n0, a.N, A4);
 #pragma unroll
         for (int k = 0; k < kNS; ++k) A4[k] *= kLog2e;
     }
     const long long seg0 = ((long long)p.b * sg.segs) * a.C + c, seg_c = (long long)a.C;
-    if (PASS == 2) wait_for_stream();
     if (live) {
         if (PASS == 2) {
             // the state before this segment: segment 0's end, through the segments in between
