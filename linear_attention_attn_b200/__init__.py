@@ -24,8 +24,8 @@ import os
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libla_b200.so")
 
-if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(_PKG, "_la_bind.so")):
-    raise ImportError("libla_b200.so and _la_bind.so are not built: run `python -m linear_attention_attn_b200.build` "
+if not os.path.exists(LIB_PATH):
+    raise ImportError("libla_b200.so is not built: run `python -m linear_attention_attn_b200.build` "
                       "(or __graft_entry__.build()) first")
 
 _lib = ctypes.CDLL(LIB_PATH)
@@ -518,7 +518,11 @@ _bind = None
 def _load_bind():
     global _bind
     import torch  # noqa: F401  (the module links against torch's libraries)
-    from . import _la_bind
+    try:
+        from . import _la_bind
+    except ImportError as e:
+        raise ImportError("the operators around the token mixers need _la_bind.so, which is not built for this Python "
+                          "and torch (%s): run `python linear_attention_attn_b200/build.py`" % e) from e
     _bind = _la_bind
     return _bind
 

@@ -2,17 +2,25 @@
 
 Run ``python -m linear_attention_attn_b200.build`` (or call ``build()``).  Each
 .cu file is compiled separately (in parallel) and linked with the static CUDA
-runtime; no GPU is needed.  csrc/la_bind.cpp, the module that hands torch tensors
-to the library's entry points, is compiled with g++ against torch's headers.  The driver API entry point used for TMA
+runtime; no GPU is needed.  The driver API entry point used for TMA
 descriptors is resolved at run time, so nothing links against libcuda.
+
+csrc/la_bind.cpp, the module that hands torch tensors to the operators around
+the token mixers, is compiled with g++ against torch's and Python's headers.
+Where one of these is missing the library is built without it, with a note on
+stderr; those operators' Python functions then say so when they are called.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
+from importlib.util import find_spec
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -56,30 +64,57 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(find_spec("torch").origin)
+
+
+def _bind_includes():
+    torch_inc = os.path.join(_torch_dir(), "include")
+    return [sysconfig.get_paths()["include"], torch_inc, os.path.join(torch_inc, "torch", "csrc", "api", "include"),
+            os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+
+
+def _bind_missing() -> str:
+    """What the binding module's build lacks here ("": nothing)."""
+    if shutil.which("g++") is None:
+        return "g++"
+    if find_spec("torch") is None:
+        return "torch"
+    for h in ("Python.h", os.path.join("torch", "csrc", "autograd", "python_variable.h"), "cuda_runtime_api.h"):
+        if not any(os.path.exists(os.path.join(d, h)) for d in _bind_includes()):
+            return h
+    return ""
+
+
+def _bind_for() -> str:
+    """The Python and torch that a binding module built here is for."""
+    return "%s torch %s %s" % (sysconfig.get_config_var("SOABI"), importlib.metadata.version("torch"), _torch_dir())
+
+
 def _compile_bind(force: bool) -> str:
     obj = os.path.join(OBJ, "la_bind.o")
+    stamp = os.path.join(OBJ, "la_bind.for")
     newest = max(os.path.getmtime(BIND_SRC), _newest(glob.glob(os.path.join(INCLUDE, "*.h"))))
-    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest:
-        return obj
-    import sysconfig
-    from importlib.util import find_spec
-    torch_inc = os.path.join(os.path.dirname(find_spec("torch").origin), "include")
-    cuda_inc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE]
-    for d in (torch_inc, os.path.join(torch_inc, "torch", "csrc", "api", "include"), cuda_inc):
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == _bind_for():
+                return obj
+    py_inc, *others = _bind_includes()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-I" + py_inc, "-I" + INCLUDE]
+    for d in others:
         cmd += ["-isystem", d]
     r = subprocess.run(cmd + ["-c", BIND_SRC, "-o", obj], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s%s" % (BIND_SRC, r.stdout, r.stderr))
+    with open(stamp, "w") as f:
+        f.write(_bind_for())
     return obj
 
 
 def _link_bind(obj: str) -> None:
-    from importlib.util import find_spec
-    torch_lib = os.path.join(os.path.dirname(find_spec("torch").origin), "lib")
     tmp = BIND + ".tmp%d" % os.getpid()
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libla_b200.so", "-Wl,-rpath,$ORIGIN", "-L" + torch_lib,
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libla_b200.so", "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
@@ -93,8 +128,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force:
         for o in glob.glob(os.path.join(OBJ, "*.o")):
             os.remove(o)
+    missing = _bind_missing()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        bind = ex.submit(_compile_bind, force)
+        bind = None if missing else ex.submit(_compile_bind, force)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
         tmp = LIB + ".tmp%d" % os.getpid()
@@ -103,6 +139,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
         os.replace(tmp, LIB)
+    if missing:
+        sys.stderr.write("%s not found: built without _la_bind.so (the operators around the token mixers from Python)\n"
+                         % missing)
+        return LIB
     obj = bind.result()
     if force or not os.path.exists(BIND) or os.path.getmtime(BIND) < os.path.getmtime(obj):
         _link_bind(obj)
