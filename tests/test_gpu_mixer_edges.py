@@ -1,4 +1,4 @@
-"""Non-finite values, outlying rows, far positions and narrow accesses of the operators around the
+"""Non-finite values, outlying rows, far positions, narrow accesses and wide rows of the operators around the
 token mixers, against their 64-bit definitions."""
 from fractions import Fraction
 
@@ -70,6 +70,59 @@ def test_group_norm_variance_behind_an_outlying_first_row(C, G):
         close(rstd[b:b + 1], wr, "rstd", 200, wr * (1 + wr * xm))
 
 
+@pytest.mark.parametrize("dtype,B,C,G", [("f32", 9, 8192, 2), ("bf16", 5, 4095, 1), ("f16", 5, 4094, 1),
+                                         ("f32", 3, 12285, 3), ("f32", 700, 2050, 1)])
+def test_group_norm_gradient_of_wide_single_rows(dtype, B, C, G):
+    """T = 1 with up to 16 vectors a thread."""
+    normal = _gen(3)
+    dt = DTYPES[dtype]
+    x, dy = normal(B, 1, C, dtype=dt), normal(B, 1, C, dtype=dt)
+    ga, be = 1 + 0.2 * normal(C), 0.2 * normal(C)
+    y, mean, rstd = torch.empty_like(x), torch.empty(B, G, device=_dev()), torch.empty(B, G, device=_dev())
+    la.la_group_norm_fwd(x, y, G, gamma=ga, beta=be, activation="silu", mean=mean, rstd=rstd)
+    leaves = [t.double().requires_grad_() for t in (x, ga, be)]
+    wy, _, wr = ref.norm(*leaves, G, 1e-5, "silu")
+    grads = torch.autograd.grad(wy, leaves, dy.double())
+    dx, dga, dbe = torch.full_like(x, NAN), torch.full_like(ga, NAN), torch.full_like(be, NAN)
+    la.la_group_norm_bwd(x, dy, dx, G, mean, rstd, gamma=ga, beta=be, dgamma=dga, dbeta=dbe, activation="silu")
+    # the bounds of the parity tests (400 and 300 + B T roundings)
+    xh = ref.norm(x.double(), None, None, G, 1e-5, "none")[0]
+    rs = wr.detach().repeat_interleave(C // G, 1)[:, None]
+    unit = ga.abs().max().double() * (rs * x.abs().max().double() * (1 + xh.abs())) + 1
+    g = 1.1 * dy.abs().double()
+    close(dx, grads[0], "dx", 400, rs * ga.abs().max().double() * g.max() * (1 + xh.abs()) * unit.amax())
+    close(dga, grads[1], "dgamma", 300 + B, (g * (xh.abs() + unit)).sum((0, 1)))
+    close(dbe, grads[2], "dbeta", 300 + B, (g * unit).sum((0, 1)))
+
+
+def _odd(t):
+    """The same values at an address that only one element divides."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    flat[1:].copy_(t.reshape(-1))
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,T,C,G", [(40, 1, 96, 4), (3, 1, 4096, 1), (2, 600, 48, 6), (2, 90, 2600, 2)])
+def test_group_norm_gradient_at_addresses_of_one_element(dtype, B, T, C, G):
+    normal = _gen(4)
+    dt = DTYPES[dtype]
+    x, dy = normal(B, T, C, dtype=dt), normal(B, T, C, dtype=dt)
+    ga = 1 + 0.2 * normal(C)
+    mean, rstd = torch.empty(B, G, device=_dev()), torch.empty(B, G, device=_dev())
+    la.la_group_norm_fwd(x, torch.empty_like(x), G, gamma=ga, mean=mean, rstd=rstd)
+    outs = []
+    for f in (lambda t: t, _odd):
+        dx, dga, dbe = f(torch.full_like(x, NAN)), f(torch.full_like(ga, NAN)), f(torch.full_like(ga, NAN))
+        la.la_group_norm_bwd(f(x), f(dy), dx, G, f(mean), f(rstd), gamma=f(ga), dgamma=dga, dbeta=dbe)
+        outs.append((dx, dga, dbe))
+    # another access width sums in another order: the bounds of the parity tests on both sides
+    (dx, dga, dbe), (dx2, dga2, dbe2) = outs
+    close(dx2, dx.double(), "dx", 800 + 2.0 ** 24 * torch.finfo(dt).eps / 2, dx.abs().max().double() + 8)
+    close(dga2, dga.double(), "dgamma", 600 + 2 * B * T, (dy.double().abs() * 6).sum((0, 1)))
+    close(dbe2, dbe.double(), "dbeta", 600 + 2 * B * T, (dy.double().abs() * 2).sum((0, 1)))
+
+
 # ------------------------------------------------------------------------------------- rotary --
 
 TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
@@ -91,6 +144,21 @@ def test_rotary_angles_of_far_positions(layout):
     want = torch.cat([u, v], -1) if layout == "half" else torch.stack([u, v], -1).flatten(-2)
     # the bound of the parity test: the angle off by pi 2^-24, the sine's own 2 roundings, two products, a sum
     close(o, want, "rotary", 12, 2.5 * q.abs().max().double())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_gradient_at_addresses_of_one_element(dtype, layout):
+    normal = _gen(5)
+    q, k = normal(2, 3, 7, 64, dtype=DTYPES[dtype]), normal(2, 1, 7, 64, dtype=DTYPES[dtype])
+    freqs = la.la_rotary_frequencies(32).to(_dev())
+    outs = []
+    for f in (lambda t: t, _odd):
+        dq, dk = f(torch.full_like(q, NAN)), f(torch.full_like(k, NAN))
+        la.la_rotary_bwd(f(q), f(k), dq, dk, f(freqs), start=77, layout=layout, magnitude=1.5)
+        outs.append((dq, dk))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------------------- convolution --
@@ -243,3 +311,20 @@ def test_selective_scan_gradient_of_infinities(T, N, skip, gate):
         ok = _same_where_not_finite(got[n], want[n], "d" + n)
         scale = want[n][ok].abs().max() if ok.any() else 1.0
         close(got[n][ok], want[n][ok], "d" + n, 2 * (24 * dy.shape[1] + 64) + dy.numel(), scale)
+
+
+def test_decays_of_small_steps_are_not_off_to_one_side():
+    """One state a channel that decays a little for 2048 tokens: averaged over channels, a decay is off by
+    at most 1.5e-8 (the unit's own truncation alone is 1.7e-8 to 2.7e-8)."""
+    B, T, C = 1, 2048, 4096
+    g = torch.Generator(device="cuda").manual_seed(10)
+    A = -(torch.rand(C, 1, generator=g, device=_dev()) * 0.9 + 0.1)
+    dt = torch.full((B, T, C), 2.0 ** -8, device=_dev())
+    x, bc = torch.zeros(B, T, C, device=_dev()), torch.zeros(B, T, 1, 1, device=_dev())
+    s = torch.ones(B, C, 1, device=_dev())
+    so = torch.empty_like(s)
+    la.la_selective_scan_fwd(x, dt, A, bc, bc, torch.empty_like(x), state_in=s, state_out=so, softplus=False)
+    off = (so.double().log()[0, :, 0] - A.double()[:, 0] * 2.0 ** -8 * T) / T
+    # a channel's decay is also rounded, by up to 2^-25, the same way at every token: over 4096 channels
+    # that averages to 2^-25 / sqrt(3 4096) = 2.7e-10, and the products' roundings to less
+    assert abs(float(off.mean())) <= 1.5e-8, float(off.mean())
