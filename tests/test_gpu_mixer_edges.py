@@ -313,18 +313,20 @@ def test_selective_scan_gradient_of_infinities(T, N, skip, gate):
         close(got[n][ok], want[n][ok], "d" + n, 2 * (24 * dy.shape[1] + 64) + dy.numel(), scale)
 
 
-def test_decays_of_small_steps_are_not_off_to_one_side():
-    """One state a channel that decays a little for 2048 tokens: averaged over channels, a decay is off by
-    at most 1.5e-8 (the unit's own truncation alone is 1.7e-8 to 2.7e-8)."""
-    B, T, C = 1, 2048, 4096
+@pytest.mark.parametrize("T,d", [(2048, 2.0 ** -8), (64, 2.0 ** -2)])
+def test_decays_are_not_off_to_one_side(T, d):
+    """One state a channel that decays by exp(-d / 10) to exp(-d 1.38) at every token: averaged over channels, the
+    decays are off by at most 1.2e-8, the bound that scan::decay2 states (the exponential unit's truncation alone
+    measures 1.65e-8 at d = 1/4)."""
+    C = 4096
     g = torch.Generator(device="cuda").manual_seed(10)
-    A = -(torch.rand(C, 1, generator=g, device=_dev()) * 0.9 + 0.1)
-    dt = torch.full((B, T, C), 2.0 ** -8, device=_dev())
-    x, bc = torch.zeros(B, T, C, device=_dev()), torch.zeros(B, T, 1, 1, device=_dev())
-    s = torch.ones(B, C, 1, device=_dev())
+    A = -(torch.rand(C, 1, generator=g, device=_dev()) * 1.28 + 0.1)
+    dt = torch.full((1, T, C), d, device=_dev())
+    x, bc = torch.zeros(1, T, C, device=_dev()), torch.zeros(1, T, 1, 1, device=_dev())
+    s = torch.ones(1, C, 1, device=_dev())
     so = torch.empty_like(s)
     la.la_selective_scan_fwd(x, dt, A, bc, bc, torch.empty_like(x), state_in=s, state_out=so, softplus=False)
-    off = (so.double().log()[0, :, 0] - A.double()[:, 0] * 2.0 ** -8 * T) / T
-    # a channel's decay is also rounded, by up to 2^-25, the same way at every token: over 4096 channels
-    # that averages to 2^-25 / sqrt(3 4096) = 2.7e-10, and the products' roundings to less
-    assert abs(float(off.mean())) <= 1.5e-8, float(off.mean())
+    off = (so.double().log()[0, :, 0] - A.double()[:, 0] * d * T) / T
+    # a channel's decay is also rounded, by up to 2^-25, the same way at every token, and so is the product with
+    # its state, by chance: over 4096 channels that averages to 2^-25 / sqrt(3 4096) = 2.7e-10 and less
+    assert abs(float(off.mean())) <= 1.2e-8, float(off.mean())
