@@ -162,8 +162,9 @@ __device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a,
 __device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
 
 // ----------------------------------------------------------- activations --
-// 1 / (1 + e^-x).  For x below about -88 the exponential overflows to infinity and the result
-// is 0; the relative error is a few 2^-22 where |x| is a few units.
+// 1 / (1 + e^-x).  Relative error 2.4e-7 down to x = -3, 1e-6 at -20, 3.8e-6 at -85 (the argument's rounding
+// grows with it, next to a result of e^x); below -87.3 the reciprocal is 0.  x sigma(x) is off by
+// less than 1e-7 for every x below 0.
 __device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
 __device__ __forceinline__ f2 sigmoid2(f2 x) {
     float a, b;

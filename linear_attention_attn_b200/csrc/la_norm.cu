@@ -15,10 +15,11 @@
 // joined through their means, sum M2_i + n_i (mean_i - mean)^2, so a mean far above the spread costs no
 // precision.  Every sum runs in a fixed order.  An infinity (which is no pivot) makes its group's mean
 // infinite, and like a NaN the variance and the whole group NaN, as the formula does.
-// B2 T65536 C640 G32 f16 with SiLU (168 MB in, 168 out): 109 us, where two reads and a write at the
+// B2 T65536 C640 G32 f16 with SiLU (168 MB in, 168 out): 107 us, where two reads and a write at the
 // measured copy bandwidth would take 77; the second launch's special-function units are 62 % busy
 // (an exponential and a reciprocal an element), the memory 50 %.  B3 T4087 C330 G30 fp32 gradient:
-// 25 us for 97 MB in three passes over 16 MB tensors, mostly the two launches' start and joins.
+// 25 us for 81 MB in five passes over tensors of 16 MB (two reads of x and dy, dx), mostly the two launches'
+// start and joins.
 #include "la_mixer.cuh"
 
 namespace la {

@@ -131,7 +131,7 @@ la_status rotary_v(const RotaryArgs &a, cudaStream_t st) {
     const long long blocks = (threads + kThreads - 1) / kThreads;
     const int heads = a.H + a.Hk;
     // Head ranges: about one wave of 148 x 8 blocks, at most one range a head.  More ranges pay for the
-    // angles again (4 waves: B8 H32 T1023 D64 f16 18.5 us instead of 12.3, B6 H40 T254 D80 R54 16.4
+    // angles again (the same inputs from call to call, so from L2; 4 waves: B8 H32 T1023 D64 f16 18.5 us instead of 12.3, B6 H40 T254 D80 R54 16.4
     // instead of 10.3; the other way only where they are few: B28 H64 T721 D36 R18 41 instead of 47).
     long long want = (148 * 8 + blocks - 1) / blocks;
     if (want > heads) want = heads;

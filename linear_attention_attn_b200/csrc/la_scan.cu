@@ -4,15 +4,15 @@
 // per channel, with d_t = softplus(dt_t + bias).
 //
 // What bounds it: one exponential for every (token, channel, state).  At N = 16 a channel's token
-// moves 8 bytes of x, dt, z and y and costs 16 exponentials; an SM makes 16 a cycle in its
-// special-function units, so they take 3 times as long as the traffic.
+// moves 8 bytes of x, dt, z and y and costs 16 exponentials and 4 special functions more (softplus, gate);
+// an SM makes 16 a cycle in its special-function units, so they take 3.5 times as long as the traffic.
 //
 // A block owns 64 / LN channels of one batch entry and walks over its tokens in tiles of 16.  The
 // rows of x, dt, z, B and C come in four elements an access, two tiles ahead, in registers; each
 // d_t, d_t x_t is formed once and left in shared memory for the LN lanes that share it; states live in
 // registers, in packed arithmetic.  Every fourth token the lanes of a channel exchange halves of
 // their four partial sums, so a sum over n costs 3 shuffles for 4 tokens.
-// Measured at B8 T4096 C2048 N16 bf16: 557 us, where the exponentials alone would take 239 and the
+// Measured at B8 T4096 C2048 N16 bf16: 557 us, where the special functions alone would take 288 and the
 // traffic 83; special-function units 53 %, issue slots 56 % busy, 3.5 warps a scheduler.  Blocks of two
 // warps (not four or one tile of 32 tokens: 560, 702 us) spread most evenly over 148 SMs.
 //
@@ -381,7 +381,9 @@ scan_step_kernel(ScanArgs a, int vec, int bvec) {
 
 // Segments of the forward, from the sizes alone: one where the (batch, channel) blocks are at least
 // four an SM; else enough for about eight an SM, each of at least 32 tokens.  Both passes run all
-// segments but one at once, so fewer than 4 segments gain nothing.
+// segments but one at once; fewer than 4 segments are not taken, although 2 or 3 gain something at 395 to
+// 591 blocks (T4096 N16 bf16, one segment against them: B1 C6400 389 and 302 us, B1 C7168 391 and 347, B2 C4096
+// 393 and 357, B1 C9216 393 and 362; fewer blocks take 4 or more).
 void fwd_segments(int B, int T, int C, int G, int N, int *segs, int *len) {
     const int width = kThreads / lanes_for(N);
     const long long blocks = (long long)B * G * ((C / G + width - 1) / width);
