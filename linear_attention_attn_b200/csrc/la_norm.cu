@@ -7,15 +7,16 @@
 //
 // Bound by HBM.  A group that fits a block's registers is read once (small kernels: a part of a
 // warp, a warp, or a block a group; mean first, then the squares about it).  A larger one takes two
-// launches over the same tiles of tokens, whole rows at a time: sums, then the result.  (Walking the
-// tiles backwards in the second, to begin with what the first left in L2, cost 2 % at B2 T65536 C640 f16
-// and 5 % in the gradient there, and changed nothing for tensors that L2 holds.)
+// launches over the same tiles of tokens, whole rows at a time: sums, then the result, the second
+// walking every tile backwards so that it begins with what the first left in L2 last.  Against forwards,
+// C640 G32 with SiLU: fp32 55 instead of 59 us at 84 MB, 100 instead of 104 at 168 (gradient 88 and 91, 157 and
+// 162); f16 68 and 67, 110 and 108 us (gradient 96 and 93, 170 and 162), where the loads are the smaller part.
 // Means and squares never meet as large sums: a thread sums about its own first value, then about the
 // mean of its first 8, 16, 32, ... values (the first may lie far from the rest), and threads and tiles are
 // joined through their means, sum M2_i + n_i (mean_i - mean)^2, so a mean far above the spread costs no
 // precision.  Every sum runs in a fixed order.  An infinity (which is no pivot) makes its group's mean
 // infinite, and like a NaN the variance and the whole group NaN, as the formula does.
-// B2 T65536 C640 G32 f16 with SiLU (168 MB in, 168 out): 107 us, where two reads and a write at the
+// B2 T65536 C640 G32 f16 with SiLU (168 MB in, 168 out): 109 us, where two reads and a write at the
 // measured copy bandwidth would take 77; the second launch's special-function units are 62 % busy
 // (an exponential and a reciprocal an element), the memory 50 %.  B3 T4087 C330 G30 fp32 gradient:
 // 25 us for 81 MB in five passes over tensors of 16 MB (two reads of x and dy, dx), mostly the two launches'
@@ -479,14 +480,14 @@ __global__ void __launch_bounds__(kTiledBlock, 2) norm_apply(NormArgs a, Tiling 
     __syncthreads();
     const int rows = at.tokens(q, at.r);
     if (rows == 0) return;
-    const long long step = (long long)q.rows * a.C;
+    const long long step = -(long long)q.rows * a.C;
     for (int v = at.v0; v < at.w; v += q.threads) {
         const L minus = by_group<V>(s_mean, v, at.cg, -1.f), rstd = by_group<V>(s_rstd, v, at.cg, 1.f);
         L ga, be;
         load_affine<V>(a, at.g0 * at.cg + v * V, ga, be);
 #pragma unroll
         for (int i = 0; i < L::n; ++i) ga.e[i] = mul(ga.e[i], rstd.e[i]);
-        long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C;
+        long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C - (rows - 1) * step;      // the last row
         batches<kRows>(rows, [&](int k, auto full) {
             constexpr bool FULL = decltype(full)::value;
             // all loads before the first store, which the compiler may not pass (y may be x)
@@ -628,14 +629,14 @@ norm_bwd_apply(NormArgs a, Tiling q, const float2 *part, const float2 *chan, uns
     __syncthreads();
     const int rows = at.tokens(q, at.r);
     if (rows == 0) return;
-    const long long step = (long long)q.rows * a.C;
+    const long long step = -(long long)q.rows * a.C;
     const float *mean = a.mean_in + (long long)at.b * a.G + at.g0, *rstd = a.rstd_in + (long long)at.b * a.G + at.g0;
     for (int v = at.v0; v < at.w; v += q.threads) {
         const L minus = by_group<V>(mean, v, at.cg, -1.f), scale = by_group<V>(rstd, v, at.cg, 1.f);
         const L m0 = by_group<V>(s_m0, v, at.cg, -1.f), m1 = by_group<V>(s_m1, v, at.cg, -1.f);
         L ga, be;
         load_affine<V>(a, at.g0 * at.cg + v * V, ga, be);
-        long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C;
+        long long o = at.base + v * V + (long long)(at.t0 + at.r) * a.C - (rows - 1) * step;      // the last row
         constexpr int U = kRows / 2;
         batches<U>(rows, [&](int k, auto full) {
             constexpr bool FULL = decltype(full)::value;
