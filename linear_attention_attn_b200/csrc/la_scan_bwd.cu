@@ -19,9 +19,10 @@
 // channel tiles in a last launch, always in the same order; that launch also joins the batch entries'
 // parts of dA, dD and dbias.
 // Measured at B4 T2048 C2048 N16 bf16: 620 us, where the traffic would take 36 and the special functions
-// (32 exponentials and 7 more a token and channel) 141; issue slots 39 % busy, shared memory 52 %: 256 blocks of four warps and 254 registers are 1.7
-// warps a scheduler.  More warps by fewer registers or segments cost more than they give (kSub = 4 with
-// 168 registers 747 us, with 128 and two segments 767; two channels a lane 980; two states a lane 806).
+// (32 exponentials and 7 more a token and channel) 141; issue slots 39 % busy, shared memory 52 %: 256 blocks
+// of four warps and 254 registers are 1.7 warps a scheduler.  More warps by fewer registers or segments cost
+// more than they give (kSub = 4 with 168 registers 747 us, with 128 and two segments 767; two channels a lane
+// 980; two states a lane 806).
 //
 // Few channels and a long sequence: segments as in the forward.  A first launch gives every
 // segment's end state from zero, S, its sum of d, and the gradient that it hands to the state
